@@ -6,11 +6,13 @@ it.  Importing the package loads nothing; the first use of a binding name import
 ``binding``, whose ``lib()`` fails loudly when the built library is missing.
 """
 _BINDING_NAMES = ("BF16", "FP16", "FP32", "INT8", "FP8E4M3", "EpError", "compress", "compress_device", "prepare",
-                  "decompress", "decompress_host", "stream_info", "lib", "StreamInfo")
+                  "decompress", "decompress_host", "stream_info", "lib", "StreamInfo", "int4_quantize",
+                  "int4_dequantize", "int4_linear", "int4_linear_dx", "int4_scale_grad", "act8_pack", "act8_unpack")
 
 
 _COMPRESSED_NAMES = ("CompressedTensor", "LatticeRANSConfig", "TileANSConfig")
-_LINEAR_NAMES = ("CompressedLinear", "CompressedFP8Linear", "CompressedINT8Linear")
+_LINEAR_NAMES = ("CompressedLinear", "CompressedFP8Linear", "CompressedINT8Linear", "GroupedINT4Linear",
+                 "int4_group_linear")
 
 
 def __getattr__(name):

@@ -138,6 +138,16 @@ def lib():
         L.ep_ans_prepare.argtypes = [C.POINTER(AnsInfo), p, p, p, p]
         L.ep_ans_decompress.restype = C.c_int
         L.ep_ans_decompress.argtypes = [C.POINTER(AnsInfo), p, p, p, p, p]
+        i32, i64 = C.c_int32, C.c_int64
+        for name, args in (("ep_int4_quantize", [p, i32, i64, i64, i64, i32, p, p, i32, p]),
+                           ("ep_int4_dequantize", [p, p, i32, i64, i64, i32, p, p]),
+                           ("ep_int4_linear", [p, p, i64, i64, i32, i32, p, i64, i64, p, p, p, p]),
+                           ("ep_int4_linear_dx", [p, p, i64, i64, i32, i32, p, i64, i64, p, p, p]),
+                           ("ep_int4_scale_grad", [p, i64, p, p, i64, p, i64, i64, i32, i32, p, p, p]),
+                           ("ep_act8_pack", [p, i32, i64, i64, i64, p, p, p]),
+                           ("ep_act8_unpack", [p, p, i64, i64, p, i32, p])):
+            getattr(L, name).restype = C.c_int
+            getattr(L, name).argtypes = args
         L.ep_status_string.restype = C.c_char_p
         L.ep_status_string.argtypes = [C.c_int]
         _lib = L
@@ -472,4 +482,227 @@ def linear_fused(x, d_blob, info, tables, bias=None, out=None, work=None, status
                            work.numel() * work.element_size(), st, s)
     if rc != 0:
         raise EpError(rc, "ep_linear_fused")
+    return out
+
+
+# ---------------------------------------------------------------- 4-bit weights with group scales
+INT4_GROUPS = (32, 64, 128)
+ACT8_GROUP = 128  # features per scale of an activation checkpoint
+
+
+class _Launch:
+    """the device and stream of one call on CUDA tensors: entering makes the device and, where the
+    caller names a stream other than the current one, that stream current (outputs made inside
+    belong to it)"""
+    __slots__ = ("index", "stream", "back", "guard")
+
+    def __init__(self, t, stream):
+        self.index = t.device.index
+        self.stream, self.back, self.guard = stream, None, None
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.index:
+            self.back = torch.cuda.current_device()
+            torch.cuda.set_device(self.index)
+        if self.stream is None:
+            return torch.cuda.current_stream(self.index).cuda_stream
+        self.guard = torch.cuda.stream(self.stream)
+        self.guard.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+def _rows(t, name, cols=None):
+    """a 2-D CUDA tensor whose rows are contiguous, with the distance between them"""
+    if t.dim() != 2 or not t.is_cuda:
+        raise EpError(-1, f"{name} must be a 2-D CUDA tensor")
+    if cols is not None and t.shape[1] != cols:
+        raise EpError(-1, f"{name} has {t.shape[1]} columns, not {cols}")
+    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        t = t.contiguous()
+    return t, (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+
+
+def _int4_weight(codes, scales, in_features, group):
+    """checks a weight's codes and scales against each other; returns out_features"""
+    if group not in INT4_GROUPS:
+        raise EpError(-1, f"group must be one of {INT4_GROUPS}, not {group}")
+    if in_features < 1:
+        raise EpError(-1, "in_features must be at least 1")
+    if codes.dtype != torch.uint8 or codes.dim() != 2 or codes.shape[1] != (in_features + 31) // 32 * 16 \
+            or codes.shape[0] < 1 or not codes.is_contiguous() or not codes.is_cuda:
+        raise EpError(-1, f"codes must be a contiguous CUDA uint8 tensor of {(in_features + 31) // 32 * 16} bytes per row")
+    if scales is not None and (scales.dtype not in (torch.bfloat16, torch.float16) or not scales.is_contiguous()
+                               or tuple(scales.shape) != (codes.shape[0], -(-in_features // group))
+                               or scales.device != codes.device):
+        raise EpError(-1, f"scales must be contiguous BF16 or FP16 of shape {(codes.shape[0], -(-in_features // group))} "
+                          "on the codes' device")
+    return codes.shape[0]
+
+
+def _output(out, shape, dtype, like, name="out"):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if out.device != like.device or out.dtype != dtype or tuple(out.shape) != tuple(shape) or not out.is_contiguous():
+        raise EpError(-1, f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {like.device}")
+    return out
+
+
+def _status(status, like):
+    if status is None:
+        return None
+    if status.device != like.device or status.dtype != torch.int32 or status.numel() < 1:
+        raise EpError(-1, "status must be an int32 tensor on the call's device")
+    return status.data_ptr()
+
+
+def int4_quantize(weight, group=128, dtype=None, stream=None):
+    """(codes, scales) of a CUDA BF16 / FP16 / FP32 (out_features, in_features) weight (ep_int4_quantize):
+    codes uint8 (out_features, ceil(in_features / 32) * 16), scales (out_features, ceil(in_features /
+    group)) of ``dtype`` (torch.bfloat16 or torch.float16; default the weight's, BF16 for FP32)."""
+    if weight.dtype not in (torch.bfloat16, torch.float16, torch.float32):
+        raise EpError(-8, f"source dtype {weight.dtype}")
+    if weight.numel() == 0:
+        raise EpError(-1, "weight must not be empty")
+    if group not in INT4_GROUPS:
+        raise EpError(-1, f"group must be one of {INT4_GROUPS}, not {group}")
+    if dtype is None:
+        dtype = torch.bfloat16 if weight.dtype == torch.float32 else weight.dtype
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise EpError(-1, f"scales are BF16 or FP16, not {dtype}")
+    if not weight.is_cuda or weight.dim() != 2:
+        raise EpError(-1, "weight must be a 2-D CUDA tensor")
+    with _Launch(weight, stream) as s:
+        w, ld = _rows(weight.detach(), "weight")
+        n, k = w.shape
+        codes = torch.empty((n, (k + 31) // 32 * 16), dtype=torch.uint8, device=w.device)
+        scales = torch.empty((n, -(-k // group)), dtype=dtype, device=w.device)
+        rc = lib().ep_int4_quantize(w.data_ptr(), CODE_OF[w.dtype], n, k, ld, group, codes.data_ptr(),
+                                    scales.data_ptr(), CODE_OF[dtype], s)
+    if rc != 0:
+        raise EpError(rc, "ep_int4_quantize")
+    return codes, scales
+
+
+def int4_dequantize(codes, scales, in_features, group=128, out=None, stream=None):
+    """the (out_features, in_features) weight s q in the scales' dtype (ep_int4_dequantize)"""
+    if scales is None:
+        raise EpError(-1, "scales are needed")
+    n = _int4_weight(codes, scales, in_features, group)
+    with _Launch(codes, stream) as s:
+        out = _output(out, (n, in_features), scales.dtype, codes)
+        rc = lib().ep_int4_dequantize(codes.data_ptr(), scales.data_ptr(), CODE_OF[scales.dtype], n, in_features, group,
+                                      out.data_ptr(), s)
+    if rc != 0:
+        raise EpError(rc, "ep_int4_dequantize")
+    return out
+
+
+def int4_linear(x, codes, scales, group=128, bias=None, out=None, status=None, stream=None):
+    """Y = X W^T (+ bias) with a 4-bit group-scaled W (ep_int4_linear).  ``x``: CUDA (m, in_features) of the
+    scales' dtype, any m, rows any distance apart; ``codes``, ``scales``: from ``int4_quantize``.  Returns
+    the contiguous (m, out_features) output."""
+    if x.dim() != 2:
+        raise EpError(-1, "x must be a 2-D CUDA tensor")
+    k = x.shape[1]
+    n = _int4_weight(codes, scales, k, group)
+    if x.dtype != scales.dtype or x.device != codes.device:
+        raise EpError(-1, f"x must be {scales.dtype} on {codes.device}, as the scales are")
+    if bias is not None and (bias.dtype != x.dtype or bias.device != x.device or tuple(bias.shape) != (n,)
+                             or not bias.is_contiguous()):
+        raise EpError(-1, f"bias must be {n} contiguous {x.dtype} elements on {x.device}")
+    with _Launch(x, stream) as s:
+        x, ld = _rows(x, "x")
+        out = _output(out, (x.shape[0], n), x.dtype, x)
+        rc = lib().ep_int4_linear(codes.data_ptr(), scales.data_ptr(), n, k, group, CODE_OF[x.dtype], x.data_ptr(),
+                                  x.shape[0], ld, None if bias is None else bias.data_ptr(), out.data_ptr(),
+                                  _status(status, x), s)
+    if rc != 0:
+        raise EpError(rc, "ep_int4_linear")
+    return out
+
+
+def int4_linear_dx(dy, codes, scales, in_features, group=128, out=None, status=None, stream=None):
+    """dX = dY W, the input gradient of ``int4_linear`` (ep_int4_linear_dx).  ``dy``: CUDA (m,
+    out_features) of the scales' dtype."""
+    if scales is None:
+        raise EpError(-1, "scales are needed")
+    n = _int4_weight(codes, scales, in_features, group)
+    if dy.dtype != scales.dtype or dy.device != codes.device:
+        raise EpError(-1, f"dy must be {scales.dtype} on {codes.device}, as the scales are")
+    with _Launch(codes, stream) as s:
+        dy, ld = _rows(dy, "dy", n)
+        out = _output(out, (dy.shape[0], in_features), dy.dtype, dy)
+        rc = lib().ep_int4_linear_dx(codes.data_ptr(), scales.data_ptr(), n, in_features, group, CODE_OF[dy.dtype],
+                                     dy.data_ptr(), dy.shape[0], ld, out.data_ptr(), _status(status, dy), s)
+    if rc != 0:
+        raise EpError(rc, "ep_int4_linear_dx")
+    return out
+
+
+def act8_pack(x, stream=None):
+    """(codes, scales) of an 8-bit checkpoint of CUDA BF16 / FP16 / FP32 (m, features) activations
+    (ep_act8_pack): codes int8 (m, ceil(features / 16) * 16), scales fp32 (m, ceil(features / 128))."""
+    if x.dtype not in (torch.bfloat16, torch.float16, torch.float32):
+        raise EpError(-8, f"source dtype {x.dtype}")
+    if x.dim() != 2 or x.shape[1] < 1 or not x.is_cuda:
+        raise EpError(-1, "x must be a 2-D CUDA tensor with at least one feature")
+    with _Launch(x, stream) as s:
+        x, ld = _rows(x.detach(), "x")
+        m, k = x.shape
+        codes = torch.empty((m, (k + 15) // 16 * 16), dtype=torch.int8, device=x.device)
+        scales = torch.empty((m, -(-k // ACT8_GROUP)), dtype=torch.float32, device=x.device)
+        rc = lib().ep_act8_pack(x.data_ptr(), CODE_OF[x.dtype], m, k, ld, codes.data_ptr(), scales.data_ptr(), s)
+    if rc != 0:
+        raise EpError(rc, "ep_act8_pack")
+    return codes, scales
+
+
+def _act8(codes, scales, features):
+    if features < 1 or codes.dtype != torch.int8 or codes.dim() != 2 or codes.shape[1] != (features + 15) // 16 * 16 \
+            or not codes.is_contiguous() or not codes.is_cuda:
+        raise EpError(-1, f"checkpoint codes must be contiguous CUDA int8 rows of {(features + 15) // 16 * 16} bytes")
+    if scales.dtype != torch.float32 or tuple(scales.shape) != (codes.shape[0], -(-features // ACT8_GROUP)) \
+            or not scales.is_contiguous() or scales.device != codes.device:
+        raise EpError(-1, f"checkpoint scales must be contiguous fp32 of shape {(codes.shape[0], -(-features // ACT8_GROUP))}")
+
+
+def act8_unpack(codes, scales, features, dtype=torch.bfloat16, out=None, stream=None):
+    """the (m, features) activations a c of a checkpoint, rounded once to ``dtype`` (ep_act8_unpack)"""
+    _act8(codes, scales, features)
+    if dtype not in (torch.bfloat16, torch.float16, torch.float32):
+        raise EpError(-8, f"output dtype {dtype}")
+    with _Launch(codes, stream) as s:
+        out = _output(out, (codes.shape[0], features), dtype, codes)
+        rc = lib().ep_act8_unpack(codes.data_ptr(), scales.data_ptr(), codes.shape[0], features, out.data_ptr(),
+                                  CODE_OF[dtype], s)
+    if rc != 0:
+        raise EpError(rc, "ep_act8_unpack")
+    return out
+
+
+def int4_scale_grad(dy, act_codes, act_scales, codes, in_features, group=128, out=None, status=None, stream=None):
+    """the gradient of every group scale of ``int4_linear`` (ep_int4_scale_grad): ``dy`` CUDA BF16 / FP16
+    (m, out_features), the forward's input as an 8-bit checkpoint (``act8_pack``), the weight's codes.
+    Returns (out_features, ceil(in_features / group)) in dy's dtype."""
+    n = _int4_weight(codes, None, in_features, group)
+    _act8(act_codes, act_scales, in_features)
+    if dy.dtype not in (torch.bfloat16, torch.float16):
+        raise EpError(-1, f"dy must be BF16 or FP16, not {dy.dtype}")
+    if dy.device != codes.device or act_codes.device != codes.device or dy.dim() != 2 \
+            or dy.shape[0] != act_codes.shape[0]:
+        raise EpError(-1, "dy, the checkpoint and the codes must be of the same tokens on one device")
+    with _Launch(codes, stream) as s:
+        dy, ld = _rows(dy, "dy", n)
+        out = _output(out, (n, -(-in_features // group)), dy.dtype, dy)
+        rc = lib().ep_int4_scale_grad(dy.data_ptr(), ld, act_codes.data_ptr(), act_scales.data_ptr(), dy.shape[0],
+                                      codes.data_ptr(), n, in_features, group, CODE_OF[dy.dtype], out.data_ptr(),
+                                      _status(status, dy), s)
+    if rc != 0:
+        raise EpError(rc, "ep_int4_scale_grad")
     return out

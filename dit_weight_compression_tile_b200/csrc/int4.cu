@@ -1,0 +1,281 @@
+// The 4-bit group-scaled weight: its quantizer and its reconstruction, and 8-bit activation checkpoints
+// (ep_int4_quantize, ep_int4_dequantize, ep_act8_pack, ep_act8_unpack).  All four read and write each
+// element once: HBM bounds them.
+#include <algorithm>
+
+#include "int4.cuh"
+
+namespace ep {
+namespace {
+
+// a load of eight consecutive elements (valid ones; the others 0) as fp32
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, int64_t valid, bool aligned, float (&v)[8]) {
+    if (aligned && valid >= 8) {
+        if constexpr (sizeof(T) == 4) {
+            const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
+            const uint32_t r[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = Elem<T>::f(uint16_t(r[i]));
+                v[2 * i + 1] = Elem<T>::f(uint16_t(r[i] >> 16));
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (sizeof(T) == 4)
+                v[i] = i < valid ? __ldg(reinterpret_cast<const float *>(p) + i) : 0.0f;
+            else
+                v[i] = i < valid ? Elem<T>::f(__ldg(reinterpret_cast<const uint16_t *>(p) + i)) : 0.0f;
+        }
+    }
+}
+
+// the largest magnitude of a group as bits (a NaN or infinity gives at least 0x7f800000): `lanes`
+// neighbouring lanes share it
+__device__ __forceinline__ uint32_t group_top(const float (&v)[8], int lanes) {
+    uint32_t u = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u = max(u, __float_as_uint(v[i]) & 0x7fffffffu);
+    for (int d = lanes / 2; d > 0; d >>= 1) u = max(u, __shfl_xor_sync(0xffffffffu, u, d));
+    return u;
+}
+
+// Checkpoint: 16 lanes hold one group of 128 features, eight each.  Scale a = max / 127 (rounded; 1 where
+// that is 0, NaN where the group has a NaN or an infinity, whose codes are 0).
+template <typename T>
+__global__ void __launch_bounds__(256) act8_pack_kernel(const T *x, int64_t ldx, uint32_t k, uint32_t groups,
+                                                        int64_t total, int8_t *codes, float *scales, bool aligned) {
+    const uint32_t l = threadIdx.x & 15u;
+    const int64_t unit = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 4;  // (token, group)
+    const bool in = unit < total;
+    const int64_t t = in ? unit / groups : 0;
+    const uint32_t g = uint32_t(in ? unit % groups : 0), k0 = g * kActGroup + l * 8;
+    float v[8];
+    load8<T>(x + t * ldx + k0, in ? int64_t(k) - k0 : 0, aligned, v);
+    const uint32_t top = group_top(v, 16);
+    float a = __fdiv_rn(__uint_as_float(top), 127.0f);
+    if (a == 0.0f) a = 1.0f;
+    const bool bad = top >= 0x7f800000u;
+    if (bad) a = __uint_as_float(0x7fffffffu);
+    const float unit_ = quotient_unit(a), s = a * unit_, inv = __frcp_rn(s);
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int c = bad ? 0 : quotient_code(v[i] * unit_, s, inv, 127.0f);
+        w[i / 4] |= (uint32_t(c) & 0xffu) << (8 * (i & 3));
+    }
+    const int64_t row = act8_row_bytes(k);
+    if (in && k0 < row) *reinterpret_cast<uint2 *>(codes + t * row + k0) = make_uint2(w[0], w[1]);
+    if (in && l == 0) scales[unit] = a;
+}
+
+// x = RNE(a c) in the output's type
+template <typename T>
+__global__ void __launch_bounds__(256) act8_unpack_kernel(const int8_t *codes, const float *scales, uint32_t k,
+                                                          uint32_t groups, int64_t total, T *out) {
+    const uint32_t chunks = (k + 7) / 8;
+    const int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (i >= total) return;
+    const int64_t t = i / chunks;
+    const uint32_t k0 = uint32_t(i % chunks) * 8;
+    const float a = __ldg(scales + t * groups + k0 / kActGroup);
+    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(codes + t * act8_row_bytes(k) + k0));
+    T *dst = out + t * int64_t(k) + k0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float v = a * float(int8_t((j < 4 ? w.x : w.y) >> (8 * (j & 3))));
+        if (k0 + j < k) {
+            if constexpr (sizeof(T) == 4)
+                dst[j] = v;
+            else
+                reinterpret_cast<uint16_t *>(dst)[j] = Elem<T>::bits(v);
+        }
+    }
+}
+
+// Weight: a lane per word of eight inputs, group / 8 neighbouring lanes per group.  Scale s = max / 7
+// rounded to fp32 and then to S (1 where that is 0, NaN with codes 0 where the group has a NaN or an
+// infinity); codes in -7 .. 7.
+template <typename T, typename S>
+__global__ void __launch_bounds__(256) int4_quantize_kernel(const T *w, int64_t ldw, uint32_t k, uint32_t group,
+                                                            uint32_t row_lanes, int64_t total, uint32_t *codes,
+                                                            S *scales, bool aligned) {
+    const int64_t id = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;  // row_lanes (a multiple of 16) per row
+    const bool in = id < total;
+    const int64_t o = in ? id / row_lanes : 0;
+    const uint32_t j = uint32_t(in ? id % row_lanes : 0), k0 = 8 * j;
+    float v[8];
+    load8<T>(w + o * ldw + k0, in ? int64_t(k) - k0 : 0, aligned, v);
+    const uint32_t lanes = group / 8, top = group_top(v, int(lanes));
+    const uint16_t sb = Elem<S>::bits(__fdiv_rn(__uint_as_float(top), 7.0f));
+    float s = Elem<S>::f(sb);
+    const bool bad = !(s < __uint_as_float(0x7f800000u));  // also a scale that overflows S
+    if (s == 0.0f) s = 1.0f;
+    if (bad) s = __uint_as_float(0x7fffffffu);
+    const float unit = quotient_unit(s), su = s * unit, inv = __frcp_rn(su);
+    uint32_t word = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int c = bad ? 0 : quotient_code(v[i] * unit, su, inv, 7.0f);
+        word |= uint32_t(c + 8) << (4 * (i / 2) + 16 * (i & 1));
+    }
+    const uint32_t words = uint32_t(int4_row_bytes(k) / 4), groups = (k + group - 1) / group;
+    if (in && j < words) codes[o * words + j] = word;
+    if (in && j % lanes == 0 && k0 < k)
+        reinterpret_cast<uint16_t *>(scales)[o * groups + j / lanes] = bad ? uint16_t(0x7fffu) : Elem<S>::bits(s);
+}
+
+// W = RNE(s q)
+template <typename S>
+__global__ void __launch_bounds__(256) int4_dequantize_kernel(const uint32_t *codes, const S *scales, uint32_t k,
+                                                              uint32_t group, int64_t total, S *out) {
+    const uint32_t used = (k + 7) / 8, words = uint32_t(int4_row_bytes(k) / 4), groups = (k + group - 1) / group;
+    const int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (i >= total) return;
+    const int64_t o = i / used;
+    const uint32_t j = uint32_t(i % used);
+    const uint32_t w = __ldg(codes + o * words + j);
+    const float s = Elem<S>::f(__ldg(reinterpret_cast<const uint16_t *>(scales) + o * groups + 8 * j / group));
+    uint16_t *dst = reinterpret_cast<uint16_t *>(out) + o * int64_t(k) + 8 * j;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (8 * j + e < k) dst[e] = Elem<S>::bits(s * float(int((w >> (4 * (e / 2) + 16 * (e & 1))) & 15u) - 8));
+}
+
+bool is16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool blocks_of(int64_t threads, unsigned *grid) {
+    const int64_t b = (threads + 255) / 256;
+    *grid = unsigned(b);
+    return b <= 0x7fffffff;
+}
+constexpr int64_t kMaxDim = int64_t(1) << 30;
+
+}  // namespace
+}  // namespace ep
+
+extern "C" int ep_act8_pack(const void *d_x, int32_t dtype, int64_t m, int64_t k, int64_t ldx, void *d_codes,
+                            float *d_scales, ep_stream_t stream) {
+    using namespace ep;
+    if (m < 0 || k < 1 || k > kMaxDim || (m > 1 && ldx < k)) return EP_ERR_INVALID_ARG;
+    if (dtype != EP_BF16 && dtype != EP_FP16 && dtype != EP_FP32) return EP_ERR_INVALID_ARG;
+    if (m == 0) return EP_OK;
+    const uint32_t elt = dtype == EP_FP32 ? 4 : 2;
+    if (!d_x || !d_codes || !d_scales || (reinterpret_cast<uintptr_t>(d_x) & (elt - 1)) || !is16(d_codes) ||
+        (reinterpret_cast<uintptr_t>(d_scales) & 3u))
+        return EP_ERR_INVALID_ARG;
+    const uint32_t groups = uint32_t((k + kActGroup - 1) / kActGroup);
+    if (m > INT64_MAX / 64 / groups) return EP_ERR_UNSUPPORTED;
+    const int64_t total = m * groups;
+    unsigned grid;
+    if (!blocks_of(total * 16, &grid)) return EP_ERR_UNSUPPORTED;
+    const bool aligned = is16(d_x) && (m == 1 || ldx * elt % 16 == 0);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    auto *c = static_cast<int8_t *>(d_codes);
+    if (dtype == EP_BF16)
+        act8_pack_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16 *>(d_x), ldx, uint32_t(k), groups, total, c,
+                                              d_scales, aligned);
+    else if (dtype == EP_FP16)
+        act8_pack_kernel<<<grid, 256, 0, s>>>(static_cast<const __half *>(d_x), ldx, uint32_t(k), groups, total, c,
+                                              d_scales, aligned);
+    else
+        act8_pack_kernel<<<grid, 256, 0, s>>>(static_cast<const float *>(d_x), ldx, uint32_t(k), groups, total, c,
+                                              d_scales, aligned);
+    return cudaGetLastError() == cudaSuccess ? EP_OK : EP_ERR_CUDA;
+}
+
+extern "C" int ep_act8_unpack(const void *d_codes, const float *d_scales, int64_t m, int64_t k, void *d_out,
+                              int32_t dtype, ep_stream_t stream) {
+    using namespace ep;
+    if (m < 0 || k < 1 || k > kMaxDim) return EP_ERR_INVALID_ARG;
+    if (dtype != EP_BF16 && dtype != EP_FP16 && dtype != EP_FP32) return EP_ERR_INVALID_ARG;
+    if (m == 0) return EP_OK;
+    const uint32_t elt = dtype == EP_FP32 ? 4 : 2;
+    if (!d_out || !d_codes || !d_scales || (reinterpret_cast<uintptr_t>(d_out) & (elt - 1)) || !is16(d_codes) ||
+        (reinterpret_cast<uintptr_t>(d_scales) & 3u))
+        return EP_ERR_INVALID_ARG;
+    const uint32_t groups = uint32_t((k + kActGroup - 1) / kActGroup), chunks = uint32_t((k + 7) / 8);
+    if (m > INT64_MAX / 64 / chunks) return EP_ERR_UNSUPPORTED;
+    const int64_t total = m * chunks;
+    unsigned grid;
+    if (!blocks_of(total, &grid)) return EP_ERR_UNSUPPORTED;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const auto *c = static_cast<const int8_t *>(d_codes);
+    if (dtype == EP_BF16)
+        act8_unpack_kernel<<<grid, 256, 0, s>>>(c, d_scales, uint32_t(k), groups, total, static_cast<__nv_bfloat16 *>(d_out));
+    else if (dtype == EP_FP16)
+        act8_unpack_kernel<<<grid, 256, 0, s>>>(c, d_scales, uint32_t(k), groups, total, static_cast<__half *>(d_out));
+    else
+        act8_unpack_kernel<<<grid, 256, 0, s>>>(c, d_scales, uint32_t(k), groups, total, static_cast<float *>(d_out));
+    return cudaGetLastError() == cudaSuccess ? EP_OK : EP_ERR_CUDA;
+}
+
+namespace ep {
+namespace {
+template <typename T>
+int quantize_from(const void *w, int64_t ldw, int64_t n, int64_t k, int32_t group, void *codes, void *scales,
+                  int32_t scale_dtype, bool aligned, cudaStream_t s) {
+    const uint32_t row_lanes = uint32_t((k + 127) / 128 * 16);
+    if (n > INT64_MAX / 64 / row_lanes) return EP_ERR_UNSUPPORTED;
+    const int64_t total = n * row_lanes;
+    unsigned grid;
+    if (!blocks_of(total, &grid)) return EP_ERR_UNSUPPORTED;
+    auto *c = static_cast<uint32_t *>(codes);
+    if (scale_dtype == EP_BF16)
+        int4_quantize_kernel<<<grid, 256, 0, s>>>(static_cast<const T *>(w), ldw, uint32_t(k), uint32_t(group), row_lanes,
+                                                  total, c, static_cast<__nv_bfloat16 *>(scales), aligned);
+    else
+        int4_quantize_kernel<<<grid, 256, 0, s>>>(static_cast<const T *>(w), ldw, uint32_t(k), uint32_t(group), row_lanes,
+                                                  total, c, static_cast<__half *>(scales), aligned);
+    return cudaGetLastError() == cudaSuccess ? EP_OK : EP_ERR_CUDA;
+}
+}  // namespace
+}  // namespace ep
+
+extern "C" int ep_int4_quantize(const void *d_w, int32_t dtype, int64_t n, int64_t k, int64_t ldw, int32_t group,
+                                void *d_codes, void *d_scales, int32_t scale_dtype, ep_stream_t stream) {
+    using namespace ep;
+    if (n < 1 || n > kMaxDim || k < 1 || k > kMaxDim || (n > 1 && ldw < k)) return EP_ERR_INVALID_ARG;
+    if (group != 32 && group != 64 && group != 128) return EP_ERR_INVALID_ARG;
+    if (dtype != EP_BF16 && dtype != EP_FP16 && dtype != EP_FP32) return EP_ERR_INVALID_ARG;
+    if (scale_dtype != EP_BF16 && scale_dtype != EP_FP16) return EP_ERR_INVALID_ARG;
+    const uint32_t elt = dtype == EP_FP32 ? 4 : 2;
+    if (!d_w || !d_codes || !d_scales || (reinterpret_cast<uintptr_t>(d_w) & (elt - 1)) || !is16(d_codes) ||
+        (reinterpret_cast<uintptr_t>(d_scales) & 1u))
+        return EP_ERR_INVALID_ARG;
+    const bool aligned = is16(d_w) && (n == 1 || ldw * elt % 16 == 0);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (dtype == EP_BF16)
+        return quantize_from<__nv_bfloat16>(d_w, ldw, n, k, group, d_codes, d_scales, scale_dtype, aligned, s);
+    if (dtype == EP_FP16)
+        return quantize_from<__half>(d_w, ldw, n, k, group, d_codes, d_scales, scale_dtype, aligned, s);
+    return quantize_from<float>(d_w, ldw, n, k, group, d_codes, d_scales, scale_dtype, aligned, s);
+}
+
+extern "C" int ep_int4_dequantize(const void *d_codes, const void *d_scales, int32_t dtype, int64_t n, int64_t k,
+                                  int32_t group, void *d_out, ep_stream_t stream) {
+    using namespace ep;
+    if (n < 1 || n > kMaxDim || k < 1 || k > kMaxDim) return EP_ERR_INVALID_ARG;
+    if (group != 32 && group != 64 && group != 128) return EP_ERR_INVALID_ARG;
+    if (dtype != EP_BF16 && dtype != EP_FP16) return EP_ERR_INVALID_ARG;
+    if (!d_codes || !d_scales || !d_out || !is16(d_codes) ||
+        ((reinterpret_cast<uintptr_t>(d_scales) | reinterpret_cast<uintptr_t>(d_out)) & 1u))
+        return EP_ERR_INVALID_ARG;
+    const uint32_t used = uint32_t((k + 7) / 8);
+    const int64_t total = n * used;
+    unsigned grid;
+    if (!blocks_of(total, &grid)) return EP_ERR_UNSUPPORTED;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const auto *c = static_cast<const uint32_t *>(d_codes);
+    if (dtype == EP_BF16)
+        int4_dequantize_kernel<<<grid, 256, 0, s>>>(c, static_cast<const __nv_bfloat16 *>(d_scales), uint32_t(k),
+                                                    uint32_t(group), total, static_cast<__nv_bfloat16 *>(d_out));
+    else
+        int4_dequantize_kernel<<<grid, 256, 0, s>>>(c, static_cast<const __half *>(d_scales), uint32_t(k),
+                                                    uint32_t(group), total, static_cast<__half *>(d_out));
+    return cudaGetLastError() == cudaSuccess ? EP_OK : EP_ERR_CUDA;
+}

@@ -13,12 +13,17 @@ the operand buffers and go no faster with more tokens, while its X slices grow).
 The FP8 / INT8 layers hold per-row absmax codes (the stream's code container) and quantize the
 activations per row of x the same way (E4M3 with scale amax / 448, INT8 with amax / 127, RNE);
 the GEMM multiplies codes and applies both scales to the fp32 / int32 products.
+
+GroupedINT4Linear holds its weight as 4-bit codes with group scales (eptile_int4.h), which need no
+entropy decode: for serving token by token, and for training the scales (and whatever comes before
+the layer) of a fixed set of codes.
 """
 import dataclasses
 
 import torch
 import torch.nn as nn
 import torch.nn.functional as F
+from torch.autograd.function import once_differentiable
 
 from . import binding as B
 from .compressed import CompressedTensor, LatticeRANSConfig, _tables, compress, decompress
@@ -240,3 +245,109 @@ class CompressedINT8Linear(_CodeLinear):
         if self.bias is not None:
             y = y + self.bias.to(y.dtype)
         return y.reshape(*shape[:-1], self.out_features)
+
+
+class _Int4GroupLinear(torch.autograd.Function):
+    """y = x W^T + b with a 4-bit group-scaled W, differentiable in x, the scales and the bias.  For the
+    scales' gradient the forward keeps its input as an 8-bit checkpoint (half the bytes of a 16-bit
+    input, and the input itself can be freed); without it nothing but the weight is kept."""
+
+    @staticmethod
+    def forward(ctx, x, codes, scales, bias, group):
+        k = x.shape[-1]
+        x2 = x.reshape(-1, k)
+        y = B.int4_linear(x2, codes, scales, group=group, bias=bias)
+        act = B.act8_pack(x2) if ctx.needs_input_grad[2] else (None, None)
+        ctx.save_for_backward(codes, scales, *act)
+        ctx.group, ctx.x_shape = group, x.shape
+        return y.reshape(*x.shape[:-1], codes.shape[0])
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        codes, scales, act_codes, act_scales = ctx.saved_tensors
+        k, dy2 = ctx.x_shape[-1], dy.reshape(-1, codes.shape[0])
+        need_x, _, need_s, need_b, _ = ctx.needs_input_grad
+        dx = B.int4_linear_dx(dy2, codes, scales, k, group=ctx.group).reshape(ctx.x_shape) if need_x else None
+        ds = B.int4_scale_grad(dy2, act_codes, act_scales, codes, k, group=ctx.group) if need_s else None
+        db = dy2.sum(0, dtype=torch.float32).to(dy.dtype) if need_b else None
+        return dx, None, ds, db, None
+
+
+def int4_group_linear(x, codes, scales, bias=None, group=128):
+    """y = x W^T (+ bias) for x (..., in_features) and a 4-bit group-scaled weight (``int4_quantize``),
+    x, scales and bias of one type (BF16 or FP16).  Differentiable in x, scales and bias; the gradient of
+    the scales is taken on the input's 8-bit checkpoint (``act8_pack``), about 1/254 of each group of 128
+    features' largest magnitude off at most per value."""
+    if not torch.is_tensor(x) or x.dim() < 1:
+        raise B.EpError(-1, "x must be a (..., in_features) tensor")
+    return _Int4GroupLinear.apply(x, codes, scales, bias, group)
+
+
+class GroupedINT4Linear(nn.Module):
+    """y = x W^T + b with W as 4-bit codes and one scale per `group` (32, 64 or 128) inputs, 4 + 16 / group
+    bits per weight.  x is a CUDA tensor of the layer's dtype (BF16 or FP16).  `train_scales` makes the
+    scales trainable (the codes stay); the bias is frozen as in the other layers unless its
+    requires_grad is set.  A layer built by the constructor holds a zero weight until quantize_weight
+    runs or a checkpoint (codes, scales, bias) is loaded."""
+
+    def __init__(self, in_features, out_features, bias=True, *, group=128, train_scales=False, device=None,
+                 dtype=torch.bfloat16):
+        super().__init__()
+        if group not in B.INT4_GROUPS:
+            raise B.EpError(-1, f"group must be one of {B.INT4_GROUPS}, not {group}")
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise B.EpError(-1, f"the layer computes in BF16 or FP16, not {dtype}")
+        if in_features < 1 or out_features < 1:
+            raise B.EpError(-1, "in_features and out_features must be at least 1")
+        self.in_features, self.out_features, self.group = in_features, out_features, group
+        self.register_buffer("codes", torch.full((out_features, (in_features + 31) // 32 * 16), 0x88, dtype=torch.uint8,
+                                                 device=device))
+        self.scales = nn.Parameter(torch.ones(out_features, -(-in_features // group), dtype=dtype, device=device),
+                                   requires_grad=train_scales)
+        self.bias = nn.Parameter(torch.zeros(out_features, device=device, dtype=dtype), requires_grad=False) \
+            if bias else None
+
+    @classmethod
+    def from_linear(cls, linear, **kwargs):
+        if linear.weight.is_meta:
+            raise B.EpError(-1, "the source weights must be loaded (not on the meta device)")
+        kwargs.setdefault("dtype", linear.weight.dtype if linear.weight.dtype == torch.float16 else torch.bfloat16)
+        layer = cls(linear.in_features, linear.out_features, bias=linear.bias is not None,
+                    device=linear.weight.device, **kwargs)
+        layer.quantize_weight(linear.weight)
+        if linear.bias is not None:
+            layer.bias.data.copy_(linear.bias.detach())
+        return layer
+
+    def quantize_weight(self, weight):
+        """the codes and scales of a CUDA BF16 / FP16 / FP32 weight (ep_int4_quantize)"""
+        if tuple(weight.shape) != (self.out_features, self.in_features):
+            raise B.EpError(-1, f"weight shape {tuple(weight.shape)} is not {(self.out_features, self.in_features)}")
+        if not weight.is_cuda:
+            raise B.EpError(-1, "the weight is quantized on the GPU: move the source layer there first")
+        codes, scales = B.int4_quantize(weight, self.group, dtype=self.scales.dtype)
+        if not bool(torch.isfinite(scales).all()):  # a group's NaN or infinity, or a scale beyond the dtype
+            raise B.EpError(-2, f"weight in groups of {self.group} with {self.scales.dtype} scales")
+        with torch.no_grad():
+            self.codes.copy_(codes)
+            self.scales.copy_(scales)
+
+    @property
+    def stored_nbytes(self):
+        """weight storage: codes and scales, excluding the bias"""
+        return self.codes.numel() + self.scales.numel() * self.scales.element_size()
+
+    @property
+    def compressed_bits(self):
+        return 8.0 * self.stored_nbytes / (self.in_features * self.out_features)
+
+    def dequantize(self):
+        return B.int4_dequantize(self.codes, self.scales.detach(), self.in_features, self.group)
+
+    def forward(self, x):
+        return int4_group_linear(x, self.codes, self.scales, self.bias, self.group)
+
+    def extra_repr(self):
+        return (f"in_features={self.in_features}, out_features={self.out_features}, bias={self.bias is not None}, "
+                f"group={self.group}")
