@@ -13,9 +13,10 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libeptile.so")
 SOURCES = ["decode.cu", "linear.cu", "device_encode.cu", "host_encode.cpp", "host_stream.cpp", "tile_ans.cu",
-           "tile_ans_host.cpp", "int4.cu", "int4_gemm.cu"]
+           "tile_ans_host.cpp", "int4.cu", "int4_gemv.cu", "int4_gemm.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("format.h", "encode_math.h", "encode_host.h", "device_util.cuh",
-                                           "decode_core.cuh", "tile_ans.h", "int4.cuh")] + \
+                                           "decode_core.cuh", "tile_ans.h", "int4.cuh",
+                                           "int4_gemm.cuh")] + \
     [os.path.join(ROOT, "include", h) for h in ("eptile.h", "eptile_int4.h")]
 
 

@@ -2,24 +2,12 @@
 // gradient (ep_int4_linear_dx) and the gradient of the group scales from an 8-bit activation
 // checkpoint (ep_int4_scale_grad).
 #include <algorithm>
+#include <atomic>
 
-#include "int4.cuh"
+#include "int4_gemm.cuh"
 
 namespace ep {
 namespace {
-
-struct Int4Args {
-    const uint32_t *codes;   // the weight's codes, words(k) per row
-    const uint16_t *scales;  // n x groups
-    const uint16_t *x;       // activations (m x k) or the output's gradient (m x n), rows ldx apart
-    const int8_t *act;       // checkpoint codes and scales
-    const float *act_scales;
-    const uint16_t *bias;
-    uint16_t *out;           // m x n, m x k or n x groups
-    int64_t ldx;
-    int64_t m;
-    uint32_t n, k, group, groups, words, act_groups;
-};
 
 enum Product { kForward, kInputGrad, kScaleGrad };
 
@@ -118,6 +106,16 @@ Int4Args args_of(int64_t n, int64_t k, int32_t group, const void *codes, const v
     a.act_groups = uint32_t((k + kActGroup - 1) / kActGroup);
     return a;
 }
+// the current device's SM count, looked up once per device
+int device_sms() {
+    static std::atomic<int> known[64];
+    int device = 0, sms = 0;
+    if (cudaGetDevice(&device) != cudaSuccess || device < 0 || device >= 64) return 0;
+    if ((sms = known[device].load()) == 0 &&
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) == cudaSuccess)
+        known[device].store(sms);
+    return sms;
+}
 template <int P>
 int launch_simple(const Int4Args &a, int32_t dtype, cudaStream_t s) {
     const int64_t I = P == kScaleGrad ? int64_t(a.n) : a.m, J = P == kForward ? a.n : a.k;
@@ -148,6 +146,10 @@ extern "C" int ep_int4_linear(const void *d_codes, const void *d_scales, int64_t
     a.m = m;
     a.bias = static_cast<const uint16_t *>(d_bias);
     a.out = static_cast<uint16_t *>(d_y);
+    a.status = d_status;
+    const int sms = device_sms();
+    if (sms < 1) return EP_ERR_CUDA;
+    if (m <= kGemvTokens) return int4_gemv(a, dtype, sms, reinterpret_cast<cudaStream_t>(stream));
     return launch_simple<kForward>(a, dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 
