@@ -21,15 +21,47 @@ struct Int4Args {
 constexpr int64_t kGemvTokens = 16;  // ep_int4_linear: up to here the weights' stream bounds it (int4_gemv.cu)
 int int4_gemv(const Int4Args &a, int32_t dtype, int sms, cudaStream_t s);
 
-// codes 2 i, 2 i + 1 of a word as a pair of exact 16-bit integers: the code's four bits below the bits of
-// 128 (BF16) or 1024 (FP16), whose last place is 1, minus 136 or 1032
+// The eight codes of a word as four pairs of exact 16-bit numbers q / 4 (BF16) or q (FP16): pair i holds
+// inputs 2 i, 2 i + 1.  Two shiftless masks, one shift, two masks, each followed by one fused
+// multiply-add:
+//   bits 0-3 under the exponent of 128 (BF16) or 1024 (FP16), where they count ones: (128 + c) / 4 - 34,
+//     1024 + c - 1032;
+//   bits 4-7: FP16 under 1024, counting 16: (1024 + 16 c) / 16 - 72.  BF16's mantissa ends at bit 6, but
+//     with a zero exponent above, bit 7 is the exponent's last place, and the subnormals and the first
+//     binade have the same spacing: the bits are the number c 2^-129; c 2^-129 2^127 - 2 = (c - 8) / 4.
+// (One shift per pair instead costs 7 integer instructions per word against 5, on the pipe that is the
+// busiest here.)
 template <typename T>
-__device__ __forceinline__ uint32_t code_pair(uint32_t word, uint32_t i) {
-    using Pair = typename Elem<T>::Pair;
-    const uint32_t v = ((word >> (4 * i)) & 0x000f000fu) | Elem<T>::kMagic;
-    const uint32_t off = Elem<T>::kMagic | 0x00080008u;
-    const Pair d = __hsub2(*reinterpret_cast<const Pair *>(&v), *reinterpret_cast<const Pair *>(&off));
-    return *reinterpret_cast<const uint32_t *>(&d);
+struct Codes;
+template <>
+struct Codes<__nv_bfloat16> {
+    static constexpr float kUnit = 4.0f;  // times this is q
+    __device__ static uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+        uint32_t d;
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+        return d;
+    }
+    __device__ static uint32_t low(uint32_t w) { return fma2((w & 0x000f000fu) | 0x43004300u, 0x3e803e80u, 0xc208c208u); }
+    __device__ static uint32_t high(uint32_t w) { return fma2(w & 0x00f000f0u, 0x7f007f00u, 0xc000c000u); }
+};
+template <>
+struct Codes<__half> {
+    static constexpr float kUnit = 1.0f;
+    __device__ static uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+        uint32_t d;
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+        return d;
+    }
+    __device__ static uint32_t low(uint32_t w) { return fma2((w & 0x000f000fu) | 0x64006400u, 0x3c003c00u, 0xe408e408u); }
+    __device__ static uint32_t high(uint32_t w) { return fma2((w & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd480d480u); }
+};
+template <typename T>
+__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&d)[4]) {
+    const uint32_t v = w >> 8;
+    d[0] = Codes<T>::low(w);
+    d[1] = Codes<T>::high(w);
+    d[2] = Codes<T>::low(v);
+    d[3] = Codes<T>::high(v);
 }
 
 // all threads of the cluster's CTAs; shared memory written before it is visible to the others after it
