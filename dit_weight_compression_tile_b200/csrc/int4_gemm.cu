@@ -1,8 +1,10 @@
 // Products with a 4-bit group-scaled weight: the linear layer's forward (ep_int4_linear), its input
 // gradient (ep_int4_linear_dx) and the gradient of the group scales from an 8-bit activation
-// checkpoint (ep_int4_scale_grad).
+// checkpoint (ep_int4_scale_grad), as tcgen05 GEMMs whose quantized operand is expanded on the way
+// from memory to the tensor cores.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "int4_gemm.cuh"
 
@@ -11,80 +13,452 @@ namespace {
 
 enum Product { kForward, kInputGrad, kScaleGrad };
 
-template <typename T>
-__device__ __forceinline__ float weight_code(const Int4Args &a, uint32_t o, uint32_t k) {
-    const uint32_t w = __ldg(a.codes + int64_t(o) * a.words + k / 8), e = k & 7u;
-    return float(int((w >> (4 * (e / 2) + 16 * (e & 1))) & 15u) - 8);
+// One CTA computes one tile of D = sum over a contraction in steps of 64:
+//   forward         D[o, t]: 128 output features x bn tokens, contraction over the inputs k
+//   input gradient  D[k, t]: 128 inputs x bn tokens, contraction over the output features o
+//   scale gradient  D[o, k]: 256 output features x 128 inputs, contraction over the tokens t
+// Roles: warps 0..7 expand the quantized operand (weight codes, or checkpoint codes in the scale
+// gradient), warp 8 issues the matrix instructions, warp 9 copies the quantized operand's bytes, warp 10
+// the dense operand (x or dy) by TMA, or warps 10..13 through registers where it is not 16-byte aligned.  Rings in shared memory:
+//   raw    the quantized operand's bytes, by TMA, 16 KB slots of four steps (scale gradient: 8 KB, one)
+//   stage  one step's operands: 16 KB expanded (16-bit), and the dense tile (bn or 4 x 64 rows of 128
+//          bytes), both rows of 64 elements with the 128-byte swizzle
+// The expanded operand's rows follow the stored codes (64 consecutive inputs of one output feature or
+// token), so the forward's W is K-major (rows o, 64 k), and the input gradient's W^T and the scale
+// gradient's x are MN-major (rows o or t, twice 64 k); dy is MN-major in the scale gradient (rows t, four
+// times 64 o).  The accumulator stays in tensor memory (bn or 256 columns).
+// Few tiles: the contraction is split over a cluster's CTAs, whose accumulators (scale gradient: group
+// sums) are joined through distributed shared memory, in rank order.
+constexpr uint32_t kExpandWarps = 8, kMmaWarp = 8, kRawWarp = 9, kDenseWarp0 = 10, kLoadWarps = 4;
+constexpr uint32_t kQuantBytes = 16384, kBarBytes = 512, kMaxStages = 8, kMaxRaws = 8;
+
+struct MmaArgs {
+    CUtensorMap dense, raw;
+    Int4Args a;
+    uint32_t bn;        // tokens of a tile (scale gradient: 128 inputs)
+    uint32_t tiles_b;   // tiles along the second index of D
+    uint32_t steps;     // of 64 along the contraction
+    uint32_t slots;     // raw slots along the contraction
+    uint32_t stages, raws, dense_bytes;
+    uint32_t idesc, tmem_cols;
+    uint32_t dense_align;  // 4 or 2 bytes, where the dense operand is not copied by TMA
+};
+
+template <int P>
+struct Shape {
+    static constexpr uint32_t kSlotSteps = P == kScaleGrad ? 1 : 4;
+    static constexpr uint32_t kRawBytes = P == kScaleGrad ? 8192 : 16384;
+};
+
+// shared-memory matrix descriptor, 128-byte swizzle: rows of 128 bytes, 8-row groups 1024 bytes apart.
+// K-major: `lead` is not used.  MN-major: each row holds 64 consecutive M (N) of one k, and `lead` is the
+// distance to the next 64.
+__device__ __forceinline__ uint64_t desc128(uint32_t addr, uint32_t lead) {
+    return uint64_t((addr >> 4) & 0x3fffu) | (uint64_t((lead >> 4) & 0x3fffu) << 16) | (uint64_t(1024 >> 4) << 32) |
+           (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
-template <typename T>
-__device__ __forceinline__ float weight_at(const Int4Args &a, uint32_t o, uint32_t k) {
-    return weight_code<T>(a, o, k) * Elem<T>::f(__ldg(a.scales + int64_t(o) * a.groups + k / a.group));
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t a, const uint32_t (&v)[4]) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+__device__ __forceinline__ void tmem_load16(uint32_t (&r)[16], uint32_t at) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-// 64 x 128 tile of D[i, j] = sum_c A(i, c) B(c, j) in fp32, 32 deep steps through shared memory, 4 x 8
-// per thread.  Forward: i token, j output feature, c input; input gradient: i token, j input, c output
-// feature; scale gradient: i output feature, j input, c token (then the tile times the codes, summed
-// over each group: 128 inputs hold whole groups).
-template <typename T, int P>
-__global__ void __launch_bounds__(256) int4_simple_kernel(const Int4Args a) {
-    __shared__ float mem[64 * 129];  // the operands' steps, then (scale gradient) the tile
-    auto sa = reinterpret_cast<float(*)[65]>(mem);
-    auto sb = reinterpret_cast<float(*)[129]>(mem + 32 * 65);
-    auto sd = reinterpret_cast<float(*)[129]>(mem);
-    const int64_t I = P == kScaleGrad ? int64_t(a.n) : a.m, C = P == kForward ? a.k : P == kInputGrad ? int64_t(a.n) : a.m;
-    const uint32_t J = P == kForward ? a.n : a.k;
-    const int64_t i0 = int64_t(blockIdx.x) * 64;
-    const uint32_t j0 = blockIdx.y * 128, ti = threadIdx.x / 16, tj = threadIdx.x % 16;
-    float d[4][8] = {};
-    for (int64_t c0 = 0; c0 < C; c0 += 32) {
-        for (uint32_t e = threadIdx.x; e < 64 * 32; e += 256) {
-            const uint32_t c = P == kScaleGrad ? e / 64 : e % 32, i = P == kScaleGrad ? e % 64 : e / 32;
-            float v = 0.0f;
-            if (i0 + i < I && c0 + c < C)
-                v = Elem<T>::f(__ldg(P == kScaleGrad ? a.x + (c0 + c) * a.ldx + i0 + i : a.x + (i0 + i) * a.ldx + c0 + c));
-            sa[c][i] = v;
-        }
-        for (uint32_t e = threadIdx.x; e < 128 * 32; e += 256) {
-            const uint32_t c = P == kForward ? e % 32 : e / 128, j = P == kForward ? e / 32 : e % 128;
-            float v = 0.0f;
-            if (j0 + j < J && c0 + c < C) {
-                if constexpr (P == kForward)
-                    v = weight_at<T>(a, j0 + j, uint32_t(c0 + c));
-                else if constexpr (P == kInputGrad)
-                    v = weight_at<T>(a, uint32_t(c0 + c), j0 + j);
-                else
-                    v = float(a.act[(c0 + c) * act8_row_bytes(a.k) + j0 + j]) *
-                        a.act_scales[(c0 + c) * a.act_groups + (j0 + j) / kActGroup];
-            }
-            sb[c][j] = v;
-        }
-        __syncthreads();
-        for (uint32_t c = 0; c < 32; ++c)
-            for (uint32_t y = 0; y < 4; ++y)
-                for (uint32_t z = 0; z < 8; ++z) d[y][z] += sa[c][ti + 16 * y] * sb[c][tj + 16 * z];
-        __syncthreads();
+// 16-bit pairs times a scale, each product rounded once
+template <typename T>
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+    using Pair = typename Elem<T>::Pair;
+    const Pair d = __hmul2(*reinterpret_cast<const Pair *>(&a), *reinterpret_cast<const Pair *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&d);
+}
+
+// Checkpoint codes: bytes 2 i, 2 i + 1 of a word as exact pairs.  BF16: the low seven bits under the
+// exponent of 128, minus 128 or (bit 7 is the exponent's last place) 256: c.  FP16: c + 128 under 1024,
+// times 1/64 minus 18: c / 64.
+// The scale comes as two 16-bit parts of a (FP16: of 64 a, so that small scales keep their digits), hi + lo;
+// c hi + (c lo) by one fused multiply-add rounds a c once but for 2^-9 (2^-12) of c lo.
+template <typename T>
+struct Act;
+template <>
+struct Act<__nv_bfloat16> {
+    static constexpr float kScale = 1.0f;
+    __device__ static uint32_t pair(uint32_t w, uint32_t i) {
+        const uint32_t p = __byte_perm(w, 0x43434343u, i ? 0x4342u : 0x4140u), mag = p & 0xff7fff7fu, off = p & 0xff80ff80u;
+        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&mag), *reinterpret_cast<const __nv_bfloat162 *>(&off));
+        return *reinterpret_cast<const uint32_t *>(&d);
     }
-    for (uint32_t y = 0; y < 4; ++y)
-        for (uint32_t z = 0; z < 8; ++z) {
-            const int64_t i = i0 + ti + 16 * y;
-            const uint32_t j = j0 + tj + 16 * z;
-            if constexpr (P == kScaleGrad) {
-                sd[ti + 16 * y][tj + 16 * z] = i < I && j < J ? d[y][z] * weight_code<T>(a, uint32_t(i), j) : 0.0f;
-            } else if (i < I && j < J) {
-                const float b = P == kForward && a.bias ? Elem<T>::f(a.bias[j]) : 0.0f;
-                a.out[i * J + j] = Elem<T>::bits(d[y][z] + b);
+};
+template <>
+struct Act<__half> {
+    static constexpr float kScale = 64.0f;
+    __device__ static uint32_t pair(uint32_t w, uint32_t i) {
+        const uint32_t p = __byte_perm(w, 0x64646464u, i ? 0x4342u : 0x4140u) ^ 0x00800080u;
+        return Codes<__half>::fma2(p, 0x24002400u, 0xcc80cc80u);  // (1024 + 128 + c) / 64 - 18
+    }
+};
+
+template <typename T, int P, bool TMA>
+__global__ void __launch_bounds__((TMA ? 11 : 14) * 32, 1) int4_mma_kernel(const __grid_constant__ MmaArgs p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    constexpr uint32_t kSlotSteps = Shape<P>::kSlotSteps, kRawBytes = Shape<P>::kRawBytes;
+    const Int4Args &a = p.a;
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+    const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+    const uint32_t stage_bytes = kQuantBytes + p.dense_bytes;
+    const uint32_t raw0 = base + p.stages * stage_bytes, bars = raw0 + p.raws * kRawBytes;
+    auto quant_full = [&](uint32_t i) { return bars + 8 * i; };
+    auto dense_full = [&](uint32_t i) { return bars + 64 + 8 * i; };
+    auto stage_free = [&](uint32_t i) { return bars + 128 + 8 * i; };
+    auto raw_full = [&](uint32_t i) { return bars + 192 + 8 * i; };
+    auto raw_free = [&](uint32_t i) { return bars + 256 + 8 * i; };
+    const uint32_t done = bars + 320, tmem_slot = bars + 328;
+    // the tile, and this CTA's share of the contraction (whole raw slots)
+    const uint32_t ta = blockIdx.x / p.tiles_b, tb = blockIdx.x % p.tiles_b;
+    const uint32_t a0 = ta * (P == kScaleGrad ? 256 : 128);  // first o (forward, scale gradient) or k
+    const int64_t b0 = int64_t(tb) * p.bn;                   // first token, or k (scale gradient)
+    const uint32_t splits = gridDim.y, rank = blockIdx.y;
+    const uint32_t slot_lo = uint32_t(uint64_t(rank) * p.slots / splits), slot_hi = uint32_t(uint64_t(rank + 1) * p.slots / splits);
+    const uint32_t step_lo = slot_lo * kSlotSteps, step_hi = min(slot_hi * kSlotSteps, p.steps);
+
+    if (threadIdx.x == 0) {
+        for (uint32_t i = 0; i < p.stages; ++i) {
+            mbar_init(quant_full(i), kExpandWarps);
+            mbar_init(dense_full(i), TMA ? 1 : kLoadWarps);
+            mbar_init(stage_free(i), 1);
+        }
+        for (uint32_t i = 0; i < p.raws; ++i) {
+            mbar_init(raw_full(i), 1);
+            mbar_init(raw_free(i), kExpandWarps);
+        }
+        mbar_init(done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_proxy_async();
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tmem_slot), "r"(p.tmem_cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = lds32(tmem_slot);
+    uint32_t err = 0;
+
+    if (warp < kExpandWarps) {
+        // ---- expand the quantized operand, 32 elements a thread and step
+        uint32_t stage = 0, phase = 0, raw = 0, raw_phase = 0;
+        for (uint32_t slot = slot_lo; slot < slot_hi && !err; ++slot) {
+            // the thread's scale of each of the slot's steps; 0 where there is none
+            uint32_t scale[kSlotSteps][P == kScaleGrad ? 2 : 1];
+#pragma unroll
+            for (uint32_t j = 0; j < kSlotSteps; ++j) {
+                const uint32_t step = slot * kSlotSteps + j;
+                if constexpr (P == kScaleGrad) {
+                    const uint32_t t = 64 * step + 32 * (warp & 1u) + lane;
+                    const float s = t < a.m ? __ldg(a.act_scales + int64_t(t) * a.act_groups + tb) * Act<T>::kScale : 0.0f;
+                    const uint32_t hi = Elem<T>::bits(s), lo = Elem<T>::bits(s - Elem<T>::f(uint16_t(hi)));
+                    scale[j][0] = hi | (hi << 16);
+                    scale[j][1] = lo | (lo << 16);
+                } else {
+                    const uint32_t o = P == kForward ? a0 + 32 * (warp & 3u) + lane : 64 * step + 32 * (warp & 1u) + lane;
+                    const uint32_t k = P == kForward ? 64 * step + 32 * (warp >> 2) : a0 + 32 * (warp >> 1);
+                    const uint32_t s = o < a.n && k < a.k ? __ldg(a.scales + int64_t(o) * a.groups + k / a.group) : 0u;
+                    scale[j][0] = s | (s << 16);
+                }
+            }
+            if (!mbar_wait(raw_full(raw), raw_phase)) {
+                err = EP_DEC_TIMEOUT;
+                break;
+            }
+            const uint32_t src = raw0 + raw * kRawBytes;
+#pragma unroll
+            for (uint32_t j = 0; j < kSlotSteps; ++j) {
+                if (slot * kSlotSteps + j >= step_hi) break;
+                uint32_t out[4][4], dst;  // four chunks of eight elements, from chunk `chunk` of row `row`
+                uint32_t row, chunk;
+                if constexpr (P == kScaleGrad) {
+                    row = 32 * (warp & 1u) + lane;
+                    const uint32_t c = warp >> 1;  // features 32 c .. of the tile's 128
+#pragma unroll
+                    for (uint32_t i = 0; i < 2; ++i) {
+                        uint32_t w[4];
+                        lds128(w, src + 128 * row + 16 * ((2 * c + i) ^ (row & 7u)));
+#pragma unroll
+                        for (uint32_t e = 0; e < 4; ++e)
+#pragma unroll
+                            for (uint32_t h = 0; h < 2; ++h) {
+                                const uint32_t v = Act<T>::pair(w[e], h);
+                                out[2 * i + e / 2][2 * (e & 1u) + h] = Codes<T>::fma2(v, scale[j][0], mul2<T>(v, scale[j][1]));
+                            }
+                    }
+                    dst = 8192 * (c >> 1);
+                    chunk = 4 * (c & 1u);
+                } else {
+                    uint32_t w[4];
+                    if constexpr (P == kForward) {
+                        row = 32 * (warp & 3u) + lane;
+                        const uint32_t h = warp >> 2;  // inputs 32 h .. of the step's 64
+                        lds128(w, src + 128 * row + 16 * ((2 * j + h) ^ (row & 7u)));
+                        dst = 0;
+                        chunk = 4 * h;
+                    } else {
+                        row = 32 * (warp & 1u) + lane;
+                        const uint32_t c = warp >> 1, r = 64 * j + row;  // inputs 32 c .. of the tile's 128
+                        lds128(w, src + 64 * r + 16 * (c ^ ((r >> 1) & 3u)));
+                        dst = 8192 * (c >> 1);
+                        chunk = 4 * (c & 1u);
+                    }
+#pragma unroll
+                    for (uint32_t i = 0; i < 4; ++i) {
+                        code_pairs<T>(w[i], out[i]);
+#pragma unroll
+                        for (uint32_t e = 0; e < 4; ++e) out[i][e] = mul2<T>(out[i][e], scale[j][0]);
+                    }
+                }
+                if (!mbar_wait(stage_free(stage), phase ^ 1u)) {
+                    err = EP_DEC_TIMEOUT;
+                    break;
+                }
+                dst += base + stage * stage_bytes + 128 * row;
+#pragma unroll
+                for (uint32_t i = 0; i < 4; ++i) sts128(dst + 16 * ((chunk + i) ^ (row & 7u)), out[i]);
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(quant_full(stage));
+                if (++stage == p.stages) stage = 0, phase ^= 1u;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(raw_free(raw));
+            if (++raw == p.raws) raw = 0, raw_phase ^= 1u;
+        }
+    } else if (warp == kRawWarp) {
+        // ---- the quantized operand's bytes, a slot ahead of need as buffers come free
+        if (lane == 0) {
+            uint32_t raw = 0, phase = 0, copies = 0;
+            for (uint32_t slot = slot_lo; slot < slot_hi; ++slot, ++copies) {
+                if (!mbar_wait(raw_free(raw), phase ^ 1u)) {
+                    err = EP_DEC_TIMEOUT;
+                    break;
+                }
+                mbar_expect(raw_full(raw), kRawBytes);
+                if constexpr (P == kForward)
+                    tma_load(raw0 + raw * kRawBytes, &p.raw, 128 * slot, a0, raw_full(raw));
+                else if constexpr (P == kInputGrad)
+                    tma_load(raw0 + raw * kRawBytes, &p.raw, a0 / 2, 256 * slot, raw_full(raw));
+                else
+                    tma_load(raw0 + raw * kRawBytes, &p.raw, uint32_t(b0), 64 * slot, raw_full(raw));
+                if (++raw == p.raws) raw = 0, phase ^= 1u;
+            }
+            // no copy is in flight when the CTA ends: the last use of each buffer
+            for (uint32_t i = copies > p.raws ? copies - p.raws : 0; i < copies; ++i)
+                if (!mbar_wait(raw_full(i % p.raws), (i / p.raws) & 1u)) err = EP_DEC_TIMEOUT;
+        }
+        __syncwarp();
+    } else if (TMA && warp == kDenseWarp0) {
+        // ---- the dense operand by TMA
+        if (lane == 0) {
+            uint32_t stage = 0, phase = 0, copies = 0;
+            for (uint32_t step = step_lo; step < step_hi; ++step, ++copies) {
+                if (!mbar_wait(stage_free(stage), phase ^ 1u)) {
+                    err = EP_DEC_TIMEOUT;
+                    break;
+                }
+                const uint32_t dst = base + stage * stage_bytes + kQuantBytes;
+                mbar_expect(dense_full(stage), p.dense_bytes);
+                if constexpr (P == kScaleGrad) {
+#pragma unroll
+                    for (uint32_t i = 0; i < 4; ++i) tma_load(dst + 8192 * i, &p.dense, a0 + 64 * i, 64 * step, dense_full(stage));
+                } else {
+                    tma_load(dst, &p.dense, 64 * step, uint32_t(b0), dense_full(stage));
+                }
+                if (++stage == p.stages) stage = 0, phase ^= 1u;
+            }
+            for (uint32_t i = copies > p.stages ? copies - p.stages : 0; i < copies; ++i)
+                if (!mbar_wait(dense_full(i % p.stages), (i / p.stages) & 1u)) err = EP_DEC_TIMEOUT;
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        // ---- the matrix instructions, 16 of the contraction each
+        uint32_t stage = 0, phase = 0;
+        for (uint32_t step = step_lo; step < step_hi; ++step) {
+            if (!mbar_wait(quant_full(stage), phase) || !mbar_wait(dense_full(stage), phase)) {
+                err = EP_DEC_TIMEOUT;
+                break;
+            }
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            if (lane == 0) {
+                const uint32_t quant = base + stage * stage_bytes, dense = quant + kQuantBytes;
+#pragma unroll
+                for (uint32_t i = 0; i < 4; ++i) {
+                    const uint32_t acc = step > step_lo || i > 0;
+                    if constexpr (P == kForward) {
+                        mma_f16(tmem, desc128(quant + 32 * i, 0), desc128(dense + 32 * i, 0), p.idesc, acc);
+                    } else if constexpr (P == kInputGrad) {
+                        mma_f16(tmem, desc128(quant + 2048 * i, 8192), desc128(dense + 32 * i, 0), p.idesc, acc);
+                    } else {
+                        const uint64_t x = desc128(quant + 2048 * i, 8192);
+                        mma_f16(tmem, desc128(dense + 2048 * i, 8192), x, p.idesc, acc);
+                        mma_f16(tmem + 128, desc128(dense + 16384 + 2048 * i, 8192), x, p.idesc, acc);
+                    }
+                }
+                mma_commit(stage_free(stage));
+            }
+            __syncwarp();
+            if (++stage == p.stages) stage = 0, phase ^= 1u;
+        }
+        if (lane == 0) mma_commit(done);
+        __syncwarp();
+    } else if (!TMA && warp >= kDenseWarp0) {
+        // ---- the dense operand through registers: 16-byte chunks of 8 elements, each checked
+        const uint32_t rows = P == kScaleGrad ? 64 : p.bn, boxes = P == kScaleGrad ? 4 : 1;
+        const uint32_t cols_all = P == kForward ? a.k : a.n;
+        uint32_t stage = 0, phase = 0;
+        for (uint32_t step = step_lo; step < step_hi; ++step) {
+            if (!mbar_wait(stage_free(stage), phase ^ 1u)) {
+                err = EP_DEC_TIMEOUT;
+                break;
+            }
+            const uint32_t dst = base + stage * stage_bytes + kQuantBytes;
+            for (uint32_t e = threadIdx.x - 32 * kDenseWarp0; e < boxes * rows * 8; e += 32 * kLoadWarps) {
+                const uint32_t c = e & 7u, r = (e >> 3) % rows, box = (e >> 3) / rows;
+                const int64_t t = (P == kScaleGrad ? 64 * int64_t(step) : b0) + r;
+                const uint32_t col = (P == kScaleGrad ? a0 + 64 * box : 64 * step) + 8 * c;
+                uint32_t v[4] = {0u, 0u, 0u, 0u};
+                if (t < a.m && col < cols_all) {
+                    const uint16_t *src = a.x + t * a.ldx + col;
+                    if (p.dense_align >= 4 && col + 8 <= cols_all) {
+#pragma unroll
+                        for (uint32_t i = 0; i < 4; ++i) v[i] = __ldg(reinterpret_cast<const uint32_t *>(src) + i);
+                    } else {
+#pragma unroll
+                        for (uint32_t i = 0; i < 4; ++i) {
+                            const uint32_t lo = col + 2 * i < cols_all ? __ldg(src + 2 * i) : 0u;
+                            const uint32_t hi = col + 2 * i + 1 < cols_all ? __ldg(src + 2 * i + 1) : 0u;
+                            v[i] = lo | (hi << 16);
+                        }
+                    }
+                }
+                sts128(dst + 8192 * box + 128 * r + 16 * (c ^ (r & 7u)), v);
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(dense_full(stage));
+            if (++stage == p.stages) stage = 0, phase ^= 1u;
+        }
+    }
+
+    // ---- the result: warps 0..7 read the accumulator (a warp reaches 32 of the 128 lanes, warp & 3)
+    const uint32_t quad = tmem + ((32u * (warp & 3u)) << 16);
+    if (warp < kExpandWarps) {
+        if (!mbar_wait(done, 0)) err = EP_DEC_TIMEOUT;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    }
+    float *joint = reinterpret_cast<float *>(smem);  // sums for the cluster, where the stages were
+    if constexpr (P == kScaleGrad) {
+        // lane: feature o; 128 columns times the codes, summed over 32 inputs, then over the group
+        const uint32_t per = 128 / a.group, half = warp >> 2, f = 128 * half + 32 * (warp & 3u) + lane, o = a0 + f;
+        if (warp < kExpandWarps) {
+            float sum[4] = {};
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) {  // 32 inputs: 16 bytes of codes
+                uint4 w = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+                const uint32_t word = uint32_t(b0) / 8 + 4 * i;
+                if (o < a.n && word < a.words) w = __ldg(reinterpret_cast<const uint4 *>(a.codes + int64_t(o) * a.words + word));
+                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (uint32_t h = 0; h < 2; ++h) {
+                    uint32_t r[16];
+                    tmem_load16(r, quad + 128 * half + 32 * i + 16 * h);
+#pragma unroll
+                    for (uint32_t e = 0; e < 16; ++e) {
+                        const uint32_t in = e & 7u, code = (ws[2 * h + e / 8] >> (4 * (in / 2) + 16 * (in & 1u))) & 15u;
+                        sum[i] = fmaf(__uint_as_float(r[e]), float(int(code) - 8), sum[i]);
+                    }
+                }
+            }
+            if (per < 4) sum[0] += sum[1], sum[2] += sum[3];
+            if (per == 2) sum[1] = sum[2];
+            if (per == 1) sum[0] += sum[2];
+            if (splits > 1) {
+#pragma unroll
+                for (uint32_t i = 0; i < 4; ++i) joint[4 * f + i] = sum[i];
+            } else if (o < a.n) {
+#pragma unroll
+                for (uint32_t i = 0; i < 4; ++i) {
+                    const uint32_t g = uint32_t(b0) / a.group + i;
+                    if (i < per && g < a.groups) a.out[int64_t(o) * a.groups + g] = Elem<T>::bits(sum[i]);
+                }
             }
         }
-    if constexpr (P == kScaleGrad) {
-        __syncthreads();
-        const uint32_t per = 128 / a.group;
-        for (uint32_t e = threadIdx.x; e < 64 * per; e += 256) {
-            const uint32_t i = e / per, g = e % per;
-            float s = 0.0f;
-            for (uint32_t j = 0; j < a.group; ++j) s += sd[i][g * a.group + j];
-            if (i0 + i < I && j0 / a.group + g < a.groups)
-                a.out[(i0 + i) * a.groups + j0 / a.group + g] = Elem<T>::bits(s);
+        if (splits > 1) {
+            cluster_sync();
+            for (uint32_t e = rank * blockDim.x + threadIdx.x; e < 256 * per; e += splits * blockDim.x) {
+                const uint32_t row = a0 + e / per, i = e % per, g = uint32_t(b0) / a.group + i;
+                float s = 0.0f;
+                for (uint32_t q = 0; q < splits; ++q) s += ld_cluster(&joint[4 * (e / per) + i], q);
+                if (row < a.n && g < a.groups) a.out[int64_t(row) * a.groups + g] = Elem<T>::bits(s);
+            }
+            cluster_sync();
         }
+    } else {
+        const uint32_t J = P == kForward ? a.n : a.k;
+        if (warp < kExpandWarps) {
+            const uint32_t f = 32 * (warp & 3u) + lane, j = a0 + f;
+            const float b = P == kForward && a.bias && j < J ? Elem<T>::f(__ldg(a.bias + j)) : 0.0f;
+            for (uint32_t c = 16 * (warp >> 2); c < p.bn; c += 32) {
+                uint32_t r[16];
+                tmem_load16(r, quad + c);
+                if (splits > 1) {
+#pragma unroll
+                    for (uint32_t i = 0; i < 16; ++i) joint[128 * (c + i) + f] = __uint_as_float(r[i]);
+                } else if (j < J) {
+#pragma unroll
+                    for (uint32_t i = 0; i < 16; ++i)
+                        if (b0 + c + i < a.m)
+                            a.out[(b0 + c + i) * J + j] = Elem<T>::bits(__uint_as_float(r[i]) * Codes<T>::kUnit + b);
+                }
+            }
+        }
+        if (splits > 1) {
+            cluster_sync();
+            const uint32_t f = threadIdx.x & 127u, j = a0 + f, rows = blockDim.x / 128;
+            if (threadIdx.x / 128 < rows && j < J) {
+                const float b = P == kForward && a.bias ? Elem<T>::f(__ldg(a.bias + j)) : 0.0f;
+                for (uint32_t c = rank * rows + threadIdx.x / 128; c < p.bn && b0 + c < a.m; c += splits * rows) {
+                    float s = 0.0f;
+                    for (uint32_t q = 0; q < splits; ++q) s += ld_cluster(&joint[128 * c + f], q);
+                    a.out[(b0 + c) * J + j] = Elem<T>::bits(s * Codes<T>::kUnit + b);
+                }
+            }
+            cluster_sync();
+        }
+    }
+    if (err && a.status && lane == 0) atomicOr(a.status, err);
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(p.tmem_cols) : "memory");
     }
 }
 
@@ -116,19 +490,112 @@ int device_sms() {
         known[device].store(sms);
     return sms;
 }
+constexpr size_t kSmemMost = 232448;
+
+// the launch: tiles, the contraction's split, rings as deep as fit
+template <typename T, int P>
+int launch_mma(const Int4Args &a, int sms, cudaStream_t s) {
+    MmaArgs p{};
+    p.a = a;
+    const int64_t contraction = P == kForward ? a.k : P == kInputGrad ? int64_t(a.n) : a.m;
+    p.steps = uint32_t((contraction + 63) / 64);
+    p.slots = (p.steps + Shape<P>::kSlotSteps - 1) / Shape<P>::kSlotSteps;
+    uint64_t tiles_a, tiles_b;
+    if (P == kScaleGrad) {
+        p.bn = 128;
+        tiles_a = (a.n + 255) / 256;
+        tiles_b = (a.k + 127) / 128;
+        p.dense_bytes = 32768;
+    } else {
+        tiles_a = ((P == kForward ? a.n : a.k) + 127) / 128;
+        tiles_b = uint64_t(a.m + 255) / 256;
+        p.bn = uint32_t(((a.m + int64_t(tiles_b) - 1) / int64_t(tiles_b) + 15) / 16 * 16);
+        p.dense_bytes = p.bn * 128;
+    }
+    if (tiles_a * tiles_b > 0x7fffffff) return EP_ERR_UNSUPPORTED;
+    p.tiles_b = uint32_t(tiles_b);
+    uint32_t splits = 1;
+    if (tiles_a * tiles_b < uint64_t(sms))
+        splits = std::max(1u, std::min({8u, uint32_t(sms / (tiles_a * tiles_b)), p.slots / (P == kScaleGrad ? 4u : 1u)}));
+    const uint32_t stage = kQuantBytes + p.dense_bytes, raw = Shape<P>::kRawBytes;
+    p.raws = P == kScaleGrad ? 3 : 2;
+    p.stages = std::min<uint32_t>(kMaxStages, uint32_t((kSmemMost - kBarBytes - p.raws * raw) / stage));
+    p.raws = std::min<uint32_t>(kMaxRaws, uint32_t((kSmemMost - kBarBytes - p.stages * stage) / raw));
+    const size_t bytes = size_t(p.stages) * stage + size_t(p.raws) * raw + kBarBytes;
+    // accumulator fp32, A and B of T; the scale gradient's operands and the input gradient's weight MN-major
+    const uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u, n = P == kScaleGrad ? 128 : p.bn;
+    p.idesc = (1u << 4) | (type << 7) | (type << 10) | (P != kForward ? 1u << 15 : 0u) | (P == kScaleGrad ? 1u << 16 : 0u) |
+              ((n >> 3) << 17) | ((128u >> 4) << 24);
+    p.tmem_cols = 32;
+    while (p.tmem_cols < (P == kScaleGrad ? 256 : p.bn)) p.tmem_cols *= 2;
+    const uint64_t dense_cols = P == kForward ? a.k : a.n;
+    const int64_t ld = a.m > 1 ? a.ldx : int64_t((dense_cols + 7) / 8 * 8);
+    const bool tma = !misaligned(a.x, 16) && ld % 8 == 0 && ld < (int64_t(1) << 38) && a.m <= 0x7fffffff;
+    p.dense_align = !misaligned(a.x, 4) && ld % 2 == 0 ? 4 : 2;
+    const CUtensorMapDataType dt = type ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const uint64_t pitch = P == kScaleGrad ? uint64_t(act8_row_bytes(a.k)) : uint64_t(a.words) * 4;
+    const void *quant = P == kScaleGrad ? static_cast<const void *>(a.act) : static_cast<const void *>(a.codes);
+    if (!tensor_map(&p.raw, quant, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, pitch, P == kScaleGrad ? uint64_t(a.m) : a.n, pitch,
+                    P == kInputGrad ? 64 : 128, P == kForward ? 128 : P == kInputGrad ? 256 : 64))
+        return EP_ERR_CUDA;
+    if (tma && !tensor_map(&p.dense, a.x, dt, 2, dense_cols, uint64_t(a.m), uint64_t(ld) * 2, 64, P == kScaleGrad ? 64 : p.bn))
+        return EP_ERR_CUDA;
+    const auto kern = tma ? int4_mma_kernel<T, P, true> : int4_mma_kernel<T, P, false>;
+    static std::atomic<uint64_t> allowed[2];  // devices on which the kernel may use kSmemMost
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess || device < 0 || device >= 64) return EP_ERR_CUDA;
+    if (!(allowed[tma].load() >> device & 1u)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemMost)) != cudaSuccess)
+            return EP_ERR_CUDA;
+        allowed[tma].fetch_or(uint64_t(1) << device);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(tiles_a * tiles_b), splits);
+    cfg.blockDim = dim3((tma ? 11 : 14) * 32);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = splits;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = splits > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
+}
 template <int P>
-int launch_simple(const Int4Args &a, int32_t dtype, cudaStream_t s) {
-    const int64_t I = P == kScaleGrad ? int64_t(a.n) : a.m, J = P == kForward ? a.n : a.k;
-    const dim3 grid(unsigned((I + 63) / 64), unsigned((J + 127) / 128));
-    if ((I + 63) / 64 > 0x7fffffff || grid.y > 65535) return EP_ERR_UNSUPPORTED;
-    if (dtype == EP_BF16)
-        int4_simple_kernel<__nv_bfloat16, P><<<grid, 256, 0, s>>>(a);
-    else
-        int4_simple_kernel<__half, P><<<grid, 256, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? EP_OK : EP_ERR_CUDA;
+int launch(const Int4Args &a, int32_t dtype, int sms, cudaStream_t s) {
+    return dtype == EP_BF16 ? launch_mma<__nv_bfloat16, P>(a, sms, s) : launch_mma<__half, P>(a, sms, s);
 }
 
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
 }  // namespace
+
+bool tensor_map(CUtensorMap *map, const void *base, CUtensorMapDataType type, uint32_t elt, uint64_t cols, uint64_t rows,
+                uint64_t pitch, uint32_t box_cols, uint32_t box_rows) {
+    static std::atomic<void *> known{nullptr};
+    void *fn = known.load();
+    if (!fn) {
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess || !fn)
+            return false;
+        known.store(fn);
+    }
+    const cuuint64_t dims[2] = {cols, rows}, strides[1] = {pitch};
+    const cuuint32_t box[2] = {box_cols, box_rows}, one[2] = {1, 1};
+    const uint32_t row = box_cols * elt;
+    const CUtensorMapSwizzle swizzle = row == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                       : row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                   : CU_TENSOR_MAP_SWIZZLE_32B;
+    return reinterpret_cast<EncodeTiled>(fn)(map, type, 2, const_cast<void *>(base), dims, strides, box, one,
+                                             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace ep
 
 extern "C" int ep_int4_linear(const void *d_codes, const void *d_scales, int64_t n, int64_t k, int32_t group,
@@ -150,7 +617,7 @@ extern "C" int ep_int4_linear(const void *d_codes, const void *d_scales, int64_t
     const int sms = device_sms();
     if (sms < 1) return EP_ERR_CUDA;
     if (m <= kGemvTokens) return int4_gemv(a, dtype, sms, reinterpret_cast<cudaStream_t>(stream));
-    return launch_simple<kForward>(a, dtype, reinterpret_cast<cudaStream_t>(stream));
+    return launch<kForward>(a, dtype, sms, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" int ep_int4_linear_dx(const void *d_codes, const void *d_scales, int64_t n, int64_t k, int32_t group,
@@ -167,7 +634,10 @@ extern "C" int ep_int4_linear_dx(const void *d_codes, const void *d_scales, int6
     a.ldx = lddy;
     a.m = m;
     a.out = static_cast<uint16_t *>(d_dx);
-    return launch_simple<kInputGrad>(a, dtype, reinterpret_cast<cudaStream_t>(stream));
+    a.status = d_status;
+    const int sms = device_sms();
+    if (sms < 1) return EP_ERR_CUDA;
+    return launch<kInputGrad>(a, dtype, sms, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" int ep_int4_scale_grad(const void *d_dy, int64_t lddy, const void *d_act, const float *d_act_scales,
@@ -187,5 +657,12 @@ extern "C" int ep_int4_scale_grad(const void *d_dy, int64_t lddy, const void *d_
     a.act = static_cast<const int8_t *>(d_act);
     a.act_scales = d_act_scales;
     a.out = static_cast<uint16_t *>(d_ds);
-    return launch_simple<kScaleGrad>(a, dtype, reinterpret_cast<cudaStream_t>(stream));
+    a.status = d_status;
+    if (m == 0)  // an empty sum
+        return cudaMemsetAsync(d_ds, 0, size_t(n) * a.groups * 2, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+                   ? EP_OK
+                   : EP_ERR_CUDA;
+    const int sms = device_sms();
+    if (sms < 1) return EP_ERR_CUDA;
+    return launch<kScaleGrad>(a, dtype, sms, reinterpret_cast<cudaStream_t>(stream));
 }

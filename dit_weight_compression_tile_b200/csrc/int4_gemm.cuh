@@ -1,5 +1,8 @@
 // What the products with a 4-bit group-scaled weight share (int4_gemm.cu, int4_gemv.cu).
 #pragma once
+#include <cuda.h>
+
+#include "device_util.cuh"
 #include "int4.cuh"
 
 namespace ep {
@@ -64,9 +67,30 @@ __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&d)[4]) {
     d[3] = Codes<T>::high(v);
 }
 
+// Tensor maps (encoded by the driver on the host, passed to kernels as parameters) of a row-major matrix
+// with rows `pitch` bytes apart (a multiple of 16, as the base address): boxes of box_cols x box_rows
+// elements with the 32-, 64- or 128-byte swizzle that fits a box's row, zeros outside the matrix.
+bool tensor_map(CUtensorMap *map, const void *base, CUtensorMapDataType type, uint32_t elt, uint64_t cols, uint64_t rows,
+                uint64_t pitch, uint32_t box_cols, uint32_t box_rows);
+
+// the box at (col, row) into shared memory, completing on an mbarrier
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, uint32_t col, uint32_t row, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(map), "r"(col), "r"(row), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void lds128(uint32_t (&v)[4], uint32_t a) {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(a));
+}
+__device__ __forceinline__ void lds64(uint32_t *v, uint32_t a) {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(a));
+}
+
 // all threads of the cluster's CTAs; shared memory written before it is visible to the others after it
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 // a float of the shared memory of the cluster's CTA `rank`, at the place of this CTA's `p`
 __device__ __forceinline__ float ld_cluster(const float *p, uint32_t rank) {
