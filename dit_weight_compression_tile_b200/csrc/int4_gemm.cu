@@ -20,7 +20,7 @@ enum Product { kForward, kInputGrad, kScaleGrad };
 // Roles: warps 0..7 expand the quantized operand (weight codes, or checkpoint codes in the scale
 // gradient), warp 8 issues the matrix instructions, warp 9 copies the quantized operand's bytes, warp 10
 // the dense operand (x or dy) by TMA, or warps 10..13 through registers where it is not 16-byte aligned.  Rings in shared memory:
-//   raw    the quantized operand's bytes, by TMA, 16 KB slots of four steps (scale gradient: 8 KB, one)
+//   raw    the quantized operand's bytes, by TMA, 16 KB slots of four steps (scale gradient: two)
 //   stage  one step's operands: 16 KB expanded (16-bit), and the dense tile (bn or 4 x 64 rows of 128
 //          bytes), both rows of 64 elements with the 128-byte swizzle
 // The expanded operand's rows follow the stored codes (64 consecutive inputs of one output feature or
@@ -46,8 +46,8 @@ struct MmaArgs {
 
 template <int P>
 struct Shape {
-    static constexpr uint32_t kSlotSteps = P == kScaleGrad ? 1 : 4;
-    static constexpr uint32_t kRawBytes = P == kScaleGrad ? 8192 : 16384;
+    static constexpr uint32_t kSlotSteps = P == kScaleGrad ? 2 : 4;
+    static constexpr uint32_t kRawBytes = 16384;
 };
 
 // shared-memory matrix descriptor, 128-byte swizzle: rows of 128 bytes, 8-row groups 1024 bytes apart.
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__((TMA ? 11 : 14) * 32, 1) int4_mma_kernel(const
 
     if (threadIdx.x == 0) {
         for (uint32_t i = 0; i < p.stages; ++i) {
-            mbar_init(quant_full(i), kExpandWarps);
+            mbar_init(quant_full(i), kExpandWarps / 2);
             mbar_init(dense_full(i), TMA ? 1 : kLoadWarps);
             mbar_init(stage_free(i), 1);
         }
@@ -165,87 +165,93 @@ __global__ void __launch_bounds__((TMA ? 11 : 14) * 32, 1) int4_mma_kernel(const
     uint32_t err = 0;
 
     if (warp < kExpandWarps) {
-        // ---- expand the quantized operand, 32 elements a thread and step
-        uint32_t stage = 0, phase = 0, raw = 0, raw_phase = 0;
-        for (uint32_t slot = slot_lo; slot < slot_hi && !err; ++slot) {
-            // the thread's scale of each of the slot's steps; 0 where there is none
-            uint32_t scale[kSlotSteps][P == kScaleGrad ? 2 : 1];
+        // ---- expand the quantized operand: warps 0..3 the even steps, 4..7 the odd ones, a row of 64 elements
+        // (128 bytes) a thread: row r of the 128, that is (forward) output feature r, or (input gradient, scale
+        // gradient) output feature or token r % 64, inputs 64 (r / 64) .. of the tile's 128
+        const uint32_t odd = warp >> 2, r = 32 * (warp & 3u) + lane, cc = r >> 6;
+        uint32_t stage = odd, phase = 0, raw = 0, raw_phase = 0;
+        uint32_t scale[kSlotSteps / 2][2];
+        // the thread's scales in a slot's steps (0 where there is none), read one slot ahead
+        auto load_scales = [&](uint32_t slot) {
 #pragma unroll
-            for (uint32_t j = 0; j < kSlotSteps; ++j) {
-                const uint32_t step = slot * kSlotSteps + j;
+            for (uint32_t j = 0; j < kSlotSteps / 2; ++j) {
+                const uint32_t step = slot * kSlotSteps + 2 * j + odd;
                 if constexpr (P == kScaleGrad) {
-                    const uint32_t t = 64 * step + 32 * (warp & 1u) + lane;
-                    const float s = t < a.m ? __ldg(a.act_scales + int64_t(t) * a.act_groups + tb) * Act<T>::kScale : 0.0f;
-                    const uint32_t hi = Elem<T>::bits(s), lo = Elem<T>::bits(s - Elem<T>::f(uint16_t(hi)));
-                    scale[j][0] = hi | (hi << 16);
-                    scale[j][1] = lo | (lo << 16);
+                    const uint32_t t = 64 * step + (r & 63u);
+                    const float s = t < a.m ? __ldg(a.act_scales + int64_t(t) * a.act_groups + tb) : 0.0f;
+                    scale[j][0] = __float_as_uint(s);
                 } else {
-                    const uint32_t o = P == kForward ? a0 + 32 * (warp & 3u) + lane : 64 * step + 32 * (warp & 1u) + lane;
-                    const uint32_t k = P == kForward ? 64 * step + 32 * (warp >> 2) : a0 + 32 * (warp >> 1);
-                    const uint32_t s = o < a.n && k < a.k ? __ldg(a.scales + int64_t(o) * a.groups + k / a.group) : 0u;
-                    scale[j][0] = s | (s << 16);
+                    const uint32_t o = P == kForward ? a0 + r : 64 * step + (r & 63u);
+                    const uint32_t k = P == kForward ? 64 * step : a0 + 64 * cc;
+                    const uint16_t *row = a.scales + int64_t(o) * a.groups;
+                    scale[j][0] = o < a.n && k < a.k ? __ldg(row + k / a.group) : 0u;
+                    scale[j][1] = o < a.n && k + 32 < a.k ? __ldg(row + (k + 32) / a.group) : 0u;
                 }
             }
+        };
+        if (slot_lo < slot_hi) load_scales(slot_lo);
+        for (uint32_t slot = slot_lo; slot < slot_hi && !err; ++slot) {
+            uint32_t now[kSlotSteps / 2][2];
+#pragma unroll
+            for (uint32_t j = 0; j < kSlotSteps / 2; ++j) now[j][0] = scale[j][0], now[j][1] = scale[j][1];
+            if (slot + 1 < slot_hi) load_scales(slot + 1);
             if (!mbar_wait(raw_full(raw), raw_phase)) {
                 err = EP_DEC_TIMEOUT;
                 break;
             }
             const uint32_t src = raw0 + raw * kRawBytes;
 #pragma unroll
-            for (uint32_t j = 0; j < kSlotSteps; ++j) {
-                if (slot * kSlotSteps + j >= step_hi) break;
-                uint32_t out[4][4], dst;  // four chunks of eight elements, from chunk `chunk` of row `row`
-                uint32_t row, chunk;
+            for (uint32_t j = 0; j < kSlotSteps / 2; ++j) {
+                const uint32_t js = 2 * j + odd;  // the step within the slot
+                if (slot * kSlotSteps + js >= step_hi) break;
+                uint32_t out[8][4];
                 if constexpr (P == kScaleGrad) {
-                    row = 32 * (warp & 1u) + lane;
-                    const uint32_t c = warp >> 1;  // features 32 c .. of the tile's 128
+                    const float s = __uint_as_float(now[j][0]) * Act<T>::kScale;
+                    uint32_t hi = Elem<T>::bits(s), lo = Elem<T>::bits(s - Elem<T>::f(uint16_t(hi)));
+                    hi |= hi << 16;
+                    lo |= lo << 16;
+                    const uint32_t row = 64 * js + (r & 63u);
+#pragma unroll
+                    for (uint32_t i = 0; i < 4; ++i) {
+                        uint32_t w[4];
+                        lds128(w, src + 128 * row + 16 * ((4 * cc + i) ^ (row & 7u)));
+#pragma unroll
+                        for (uint32_t e = 0; e < 8; ++e) {
+                            const uint32_t v = Act<T>::pair(w[e / 2], e & 1u);
+                            out[2 * i + e / 4][e & 3u] = Codes<T>::fma2(v, hi, mul2<T>(v, lo));
+                        }
+                    }
+                } else {
 #pragma unroll
                     for (uint32_t i = 0; i < 2; ++i) {
                         uint32_t w[4];
-                        lds128(w, src + 128 * row + 16 * ((2 * c + i) ^ (row & 7u)));
+                        if constexpr (P == kForward) {
+                            lds128(w, src + 128 * r + 16 * ((2 * js + i) ^ (r & 7u)));
+                        } else {
+                            const uint32_t row = 64 * js + (r & 63u);
+                            lds128(w, src + 64 * row + 16 * ((2 * cc + i) ^ ((row >> 1) & 3u)));
+                        }
+                        const uint32_t s2 = now[j][i] | (now[j][i] << 16);
 #pragma unroll
-                        for (uint32_t e = 0; e < 4; ++e)
+                        for (uint32_t e = 0; e < 4; ++e) {
+                            code_pairs<T>(w[e], out[4 * i + e]);
 #pragma unroll
-                            for (uint32_t h = 0; h < 2; ++h) {
-                                const uint32_t v = Act<T>::pair(w[e], h);
-                                out[2 * i + e / 2][2 * (e & 1u) + h] = Codes<T>::fma2(v, scale[j][0], mul2<T>(v, scale[j][1]));
-                            }
-                    }
-                    dst = 8192 * (c >> 1);
-                    chunk = 4 * (c & 1u);
-                } else {
-                    uint32_t w[4];
-                    if constexpr (P == kForward) {
-                        row = 32 * (warp & 3u) + lane;
-                        const uint32_t h = warp >> 2;  // inputs 32 h .. of the step's 64
-                        lds128(w, src + 128 * row + 16 * ((2 * j + h) ^ (row & 7u)));
-                        dst = 0;
-                        chunk = 4 * h;
-                    } else {
-                        row = 32 * (warp & 1u) + lane;
-                        const uint32_t c = warp >> 1, r = 64 * j + row;  // inputs 32 c .. of the tile's 128
-                        lds128(w, src + 64 * r + 16 * (c ^ ((r >> 1) & 3u)));
-                        dst = 8192 * (c >> 1);
-                        chunk = 4 * (c & 1u);
-                    }
-#pragma unroll
-                    for (uint32_t i = 0; i < 4; ++i) {
-                        code_pairs<T>(w[i], out[i]);
-#pragma unroll
-                        for (uint32_t e = 0; e < 4; ++e) out[i][e] = mul2<T>(out[i][e], scale[j][0]);
+                            for (uint32_t h = 0; h < 4; ++h) out[4 * i + e][h] = mul2<T>(out[4 * i + e][h], s2);
+                        }
                     }
                 }
                 if (!mbar_wait(stage_free(stage), phase ^ 1u)) {
                     err = EP_DEC_TIMEOUT;
                     break;
                 }
-                dst += base + stage * stage_bytes + 128 * row;
+                const uint32_t dst = base + stage * stage_bytes + 128 * r;
 #pragma unroll
-                for (uint32_t i = 0; i < 4; ++i) sts128(dst + 16 * ((chunk + i) ^ (row & 7u)), out[i]);
+                for (uint32_t i = 0; i < 8; ++i) sts128(dst + 16 * (i ^ (r & 7u)), out[i]);
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(quant_full(stage));
-                if (++stage == p.stages) stage = 0, phase ^= 1u;
+                stage += 2;
+                if (stage >= p.stages) stage -= p.stages, phase ^= 1u;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(raw_free(raw));
@@ -266,7 +272,7 @@ __global__ void __launch_bounds__((TMA ? 11 : 14) * 32, 1) int4_mma_kernel(const
                 else if constexpr (P == kInputGrad)
                     tma_load(raw0 + raw * kRawBytes, &p.raw, a0 / 2, 256 * slot, raw_full(raw));
                 else
-                    tma_load(raw0 + raw * kRawBytes, &p.raw, uint32_t(b0), 64 * slot, raw_full(raw));
+                    tma_load(raw0 + raw * kRawBytes, &p.raw, uint32_t(b0), 128 * slot, raw_full(raw));
                 if (++raw == p.raws) raw = 0, phase ^= 1u;
             }
             // no copy is in flight when the CTA ends: the last use of each buffer
@@ -516,9 +522,9 @@ int launch_mma(const Int4Args &a, int sms, cudaStream_t s) {
     p.tiles_b = uint32_t(tiles_b);
     uint32_t splits = 1;
     if (tiles_a * tiles_b < uint64_t(sms))
-        splits = std::max(1u, std::min({8u, uint32_t(sms / (tiles_a * tiles_b)), p.slots / (P == kScaleGrad ? 4u : 1u)}));
+        splits = std::max(1u, std::min({8u, uint32_t(sms / (tiles_a * tiles_b)), p.slots / (P == kScaleGrad ? 2u : 1u)}));
     const uint32_t stage = kQuantBytes + p.dense_bytes, raw = Shape<P>::kRawBytes;
-    p.raws = P == kScaleGrad ? 3 : 2;
+    p.raws = 2;
     p.stages = std::min<uint32_t>(kMaxStages, uint32_t((kSmemMost - kBarBytes - p.raws * raw) / stage));
     p.raws = std::min<uint32_t>(kMaxRaws, uint32_t((kSmemMost - kBarBytes - p.stages * stage) / raw));
     const size_t bytes = size_t(p.stages) * stage + size_t(p.raws) * raw + kBarBytes;
@@ -536,7 +542,7 @@ int launch_mma(const Int4Args &a, int sms, cudaStream_t s) {
     const uint64_t pitch = P == kScaleGrad ? uint64_t(act8_row_bytes(a.k)) : uint64_t(a.words) * 4;
     const void *quant = P == kScaleGrad ? static_cast<const void *>(a.act) : static_cast<const void *>(a.codes);
     if (!tensor_map(&p.raw, quant, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, pitch, P == kScaleGrad ? uint64_t(a.m) : a.n, pitch,
-                    P == kInputGrad ? 64 : 128, P == kForward ? 128 : P == kInputGrad ? 256 : 64))
+                    P == kInputGrad ? 64 : 128, P == kInputGrad ? 256 : 128))
         return EP_ERR_CUDA;
     if (tma && !tensor_map(&p.dense, a.x, dt, 2, dense_cols, uint64_t(a.m), uint64_t(ld) * 2, 64, P == kScaleGrad ? 64 : p.bn))
         return EP_ERR_CUDA;
@@ -591,9 +597,18 @@ bool tensor_map(CUtensorMap *map, const void *base, CUtensorMapDataType type, ui
     const CUtensorMapSwizzle swizzle = row == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
                                        : row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                                                    : CU_TENSOR_MAP_SWIZZLE_32B;
-    return reinterpret_cast<EncodeTiled>(fn)(map, type, 2, const_cast<void *>(base), dims, strides, box, one,
-                                             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const auto encode = [&] {
+        return reinterpret_cast<EncodeTiled>(fn)(map, type, 2, const_cast<void *>(base), dims, strides, box, one,
+                                                 CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult rc = encode();
+    if (rc == CUDA_ERROR_INVALID_CONTEXT || rc == CUDA_ERROR_NOT_INITIALIZED) {
+        // a thread that has made no runtime call that binds the device's context (autograd's, say)
+        int device;
+        if (cudaGetDevice(&device) == cudaSuccess && cudaSetDevice(device) == cudaSuccess) rc = encode();
+    }
+    return rc == CUDA_SUCCESS;
 }
 
 }  // namespace ep
