@@ -16,10 +16,10 @@ enum Product { kForward, kInputGrad, kScaleGrad };
 // One CTA computes one tile of D = sum over a contraction in steps of 64:
 //   forward         D[o, t]: 128 output features x bn tokens, contraction over the inputs k
 //   input gradient  D[k, t]: 128 inputs x bn tokens, contraction over the output features o
-//   scale gradient  D[o, k]: 256 output features x 128 inputs, contraction over the tokens t
-// Roles: warps 0..7 expand the quantized operand (weight codes, or checkpoint codes in the scale
-// gradient), warp 8 issues the matrix instructions, warp 9 copies the quantized operand's bytes, warp 10
-// the dense operand (x or dy) by TMA, or warps 10..13 through registers where it is not 16-byte aligned.  Rings in shared memory:
+//   scale gradient  D[k, o]: 128 inputs x 256 output features, contraction over the tokens t
+// Roles: warps 0..15 expand the quantized operand (weight codes, or checkpoint codes in the scale
+// gradient), warp 16 issues the matrix instructions, warp 17 copies the quantized operand's bytes, warp 18
+// the dense operand (x or dy) by TMA, or warps 18..21 through registers where it is not 16-byte aligned.  Rings in shared memory:
 //   raw    the quantized operand's bytes, by TMA, 16 KB slots of four steps (scale gradient: two)
 //   stage  one step's operands: 16 KB expanded (16-bit), and the dense tile (bn or 4 x 64 rows of 128
 //          bytes), both rows of 64 elements with the 128-byte swizzle
@@ -29,7 +29,8 @@ enum Product { kForward, kInputGrad, kScaleGrad };
 // times 64 o).  The accumulator stays in tensor memory (bn or 256 columns).
 // Few tiles: the contraction is split over a cluster's CTAs, whose accumulators (scale gradient: group
 // sums) are joined through distributed shared memory, in rank order.
-constexpr uint32_t kExpandWarps = 8, kMmaWarp = 8, kRawWarp = 9, kDenseWarp0 = 10, kLoadWarps = 4;
+constexpr uint32_t kGroups = 4, kExpandWarps = 4 * kGroups, kMmaWarp = kExpandWarps, kRawWarp = kMmaWarp + 1;
+constexpr uint32_t kDenseWarp0 = kRawWarp + 1, kLoadWarps = 4;
 constexpr uint32_t kQuantBytes = 16384, kBarBytes = 512, kMaxStages = 8, kMaxRaws = 8;
 
 struct MmaArgs {
@@ -117,7 +118,7 @@ struct Act<__half> {
 };
 
 template <typename T, int P, bool TMA>
-__global__ void __launch_bounds__((TMA ? 11 : 14) * 32, 1) int4_mma_kernel(const __grid_constant__ MmaArgs p) {
+__global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1) int4_mma_kernel(const __grid_constant__ MmaArgs p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr uint32_t kSlotSteps = Shape<P>::kSlotSteps, kRawBytes = Shape<P>::kRawBytes;
     const Int4Args &a = p.a;
@@ -141,13 +142,13 @@ __global__ void __launch_bounds__((TMA ? 11 : 14) * 32, 1) int4_mma_kernel(const
 
     if (threadIdx.x == 0) {
         for (uint32_t i = 0; i < p.stages; ++i) {
-            mbar_init(quant_full(i), kExpandWarps / 2);
+            mbar_init(quant_full(i), 4);
             mbar_init(dense_full(i), TMA ? 1 : kLoadWarps);
             mbar_init(stage_free(i), 1);
         }
         for (uint32_t i = 0; i < p.raws; ++i) {
             mbar_init(raw_full(i), 1);
-            mbar_init(raw_free(i), kExpandWarps);
+            mbar_init(raw_free(i), 4 * kSlotSteps);
         }
         mbar_init(done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -165,97 +166,84 @@ __global__ void __launch_bounds__((TMA ? 11 : 14) * 32, 1) int4_mma_kernel(const
     uint32_t err = 0;
 
     if (warp < kExpandWarps) {
-        // ---- expand the quantized operand: warps 0..3 the even steps, 4..7 the odd ones, a row of 64 elements
+        // ---- expand the quantized operand: group warp / 4 takes every kGroups-th step, a row of 64 elements
         // (128 bytes) a thread: row r of the 128, that is (forward) output feature r, or (input gradient, scale
         // gradient) output feature or token r % 64, inputs 64 (r / 64) .. of the tile's 128
-        const uint32_t odd = warp >> 2, r = 32 * (warp & 3u) + lane, cc = r >> 6;
-        uint32_t stage = odd, phase = 0, raw = 0, raw_phase = 0;
-        uint32_t scale[kSlotSteps / 2][2];
-        // the thread's scales in a slot's steps (0 where there is none), read one slot ahead
-        auto load_scales = [&](uint32_t slot) {
-#pragma unroll
-            for (uint32_t j = 0; j < kSlotSteps / 2; ++j) {
-                const uint32_t step = slot * kSlotSteps + 2 * j + odd;
-                if constexpr (P == kScaleGrad) {
-                    const uint32_t t = 64 * step + (r & 63u);
-                    const float s = t < a.m ? __ldg(a.act_scales + int64_t(t) * a.act_groups + tb) : 0.0f;
-                    scale[j][0] = __float_as_uint(s);
-                } else {
-                    const uint32_t o = P == kForward ? a0 + r : 64 * step + (r & 63u);
-                    const uint32_t k = P == kForward ? 64 * step : a0 + 64 * cc;
-                    const uint16_t *row = a.scales + int64_t(o) * a.groups;
-                    scale[j][0] = o < a.n && k < a.k ? __ldg(row + k / a.group) : 0u;
-                    scale[j][1] = o < a.n && k + 32 < a.k ? __ldg(row + (k + 32) / a.group) : 0u;
-                }
+        const uint32_t group = warp >> 2, r = 32 * (warp & 3u) + lane, cc = r >> 6, steps = step_hi - step_lo;
+        uint32_t stage = group, phase = 0;
+        uint32_t scale[2];
+        // the thread's scales in a step (0 where there is none), read one step ahead
+        auto load_scales = [&](uint32_t step) {
+            if constexpr (P == kScaleGrad) {
+                const uint32_t t = 64 * step + (r & 63u);
+                scale[0] = t < a.m ? __float_as_uint(__ldg(a.act_scales + int64_t(t) * a.act_groups + tb)) : 0u;
+            } else {
+                const uint32_t o = P == kForward ? a0 + r : 64 * step + (r & 63u);
+                const uint32_t k = P == kForward ? 64 * step : a0 + 64 * cc;
+                const uint16_t *row = a.scales + int64_t(o) * a.groups;
+                scale[0] = o < a.n && k < a.k ? __ldg(row + k / a.group) : 0u;
+                scale[1] = o < a.n && k + 32 < a.k ? __ldg(row + (k + 32) / a.group) : 0u;
             }
         };
-        if (slot_lo < slot_hi) load_scales(slot_lo);
-        for (uint32_t slot = slot_lo; slot < slot_hi && !err; ++slot) {
-            uint32_t now[kSlotSteps / 2][2];
-#pragma unroll
-            for (uint32_t j = 0; j < kSlotSteps / 2; ++j) now[j][0] = scale[j][0], now[j][1] = scale[j][1];
-            if (slot + 1 < slot_hi) load_scales(slot + 1);
-            if (!mbar_wait(raw_full(raw), raw_phase)) {
+        if (group < steps) load_scales(step_lo + group);
+        for (uint32_t n = group; n < steps; n += kGroups) {  // steps counted from this CTA's first
+            const uint32_t slot = n / kSlotSteps, js = n % kSlotSteps, raw = slot % p.raws;
+            const uint32_t now[2] = {scale[0], scale[1]};
+            if (n + kGroups < steps) load_scales(step_lo + n + kGroups);
+            if (!mbar_wait(raw_full(raw), (slot / p.raws) & 1u)) {
                 err = EP_DEC_TIMEOUT;
                 break;
             }
             const uint32_t src = raw0 + raw * kRawBytes;
+            uint32_t out[8][4];
+            if constexpr (P == kScaleGrad) {
+                const float s = __uint_as_float(now[0]) * Act<T>::kScale;
+                uint32_t hi = Elem<T>::bits(s), lo = Elem<T>::bits(s - Elem<T>::f(uint16_t(hi)));
+                hi |= hi << 16;
+                lo |= lo << 16;
+                const uint32_t row = 64 * js + (r & 63u);
 #pragma unroll
-            for (uint32_t j = 0; j < kSlotSteps / 2; ++j) {
-                const uint32_t js = 2 * j + odd;  // the step within the slot
-                if (slot * kSlotSteps + js >= step_hi) break;
-                uint32_t out[8][4];
-                if constexpr (P == kScaleGrad) {
-                    const float s = __uint_as_float(now[j][0]) * Act<T>::kScale;
-                    uint32_t hi = Elem<T>::bits(s), lo = Elem<T>::bits(s - Elem<T>::f(uint16_t(hi)));
-                    hi |= hi << 16;
-                    lo |= lo << 16;
-                    const uint32_t row = 64 * js + (r & 63u);
+                for (uint32_t i = 0; i < 4; ++i) {
+                    uint32_t w[4];
+                    lds128(w, src + 128 * row + 16 * ((4 * cc + i) ^ (row & 7u)));
 #pragma unroll
-                    for (uint32_t i = 0; i < 4; ++i) {
-                        uint32_t w[4];
-                        lds128(w, src + 128 * row + 16 * ((4 * cc + i) ^ (row & 7u)));
-#pragma unroll
-                        for (uint32_t e = 0; e < 8; ++e) {
-                            const uint32_t v = Act<T>::pair(w[e / 2], e & 1u);
-                            out[2 * i + e / 4][e & 3u] = Codes<T>::fma2(v, hi, mul2<T>(v, lo));
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (uint32_t i = 0; i < 2; ++i) {
-                        uint32_t w[4];
-                        if constexpr (P == kForward) {
-                            lds128(w, src + 128 * r + 16 * ((2 * js + i) ^ (r & 7u)));
-                        } else {
-                            const uint32_t row = 64 * js + (r & 63u);
-                            lds128(w, src + 64 * row + 16 * ((2 * cc + i) ^ ((row >> 1) & 3u)));
-                        }
-                        const uint32_t s2 = now[j][i] | (now[j][i] << 16);
-#pragma unroll
-                        for (uint32_t e = 0; e < 4; ++e) {
-                            code_pairs<T>(w[e], out[4 * i + e]);
-#pragma unroll
-                            for (uint32_t h = 0; h < 4; ++h) out[4 * i + e][h] = mul2<T>(out[4 * i + e][h], s2);
-                        }
+                    for (uint32_t e = 0; e < 8; ++e) {
+                        const uint32_t v = Act<T>::pair(w[e / 2], e & 1u);
+                        out[2 * i + e / 4][e & 3u] = Codes<T>::fma2(v, hi, mul2<T>(v, lo));
                     }
                 }
-                if (!mbar_wait(stage_free(stage), phase ^ 1u)) {
-                    err = EP_DEC_TIMEOUT;
-                    break;
-                }
-                const uint32_t dst = base + stage * stage_bytes + 128 * r;
+            } else {
 #pragma unroll
-                for (uint32_t i = 0; i < 8; ++i) sts128(dst + 16 * (i ^ (r & 7u)), out[i]);
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(quant_full(stage));
-                stage += 2;
-                if (stage >= p.stages) stage -= p.stages, phase ^= 1u;
+                for (uint32_t i = 0; i < 2; ++i) {
+                    uint32_t w[4];
+                    if constexpr (P == kForward) {
+                        lds128(w, src + 128 * r + 16 * ((2 * js + i) ^ (r & 7u)));
+                    } else {
+                        const uint32_t row = 64 * js + (r & 63u);
+                        lds128(w, src + 64 * row + 16 * ((2 * cc + i) ^ ((row >> 1) & 3u)));
+                    }
+                    const uint32_t s2 = now[i] | (now[i] << 16);
+#pragma unroll
+                    for (uint32_t e = 0; e < 4; ++e) {
+                        code_pairs<T>(w[e], out[4 * i + e]);
+#pragma unroll
+                        for (uint32_t h = 0; h < 4; ++h) out[4 * i + e][h] = mul2<T>(out[4 * i + e][h], s2);
+                    }
+                }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(raw_free(raw));
-            if (++raw == p.raws) raw = 0, raw_phase ^= 1u;
+            if (!mbar_wait(stage_free(stage), phase ^ 1u)) {
+                err = EP_DEC_TIMEOUT;
+                break;
+            }
+            const uint32_t dst = base + stage * stage_bytes + 128 * r;
+#pragma unroll
+            for (uint32_t i = 0; i < 8; ++i) sts128(dst + 16 * (i ^ (r & 7u)), out[i]);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(quant_full(stage));
+            for (stage += kGroups; stage >= p.stages; stage -= p.stages) phase ^= 1u;
         }
     } else if (warp == kRawWarp) {
         // ---- the quantized operand's bytes, a slot ahead of need as buffers come free
@@ -322,9 +310,7 @@ __global__ void __launch_bounds__((TMA ? 11 : 14) * 32, 1) int4_mma_kernel(const
                     } else if constexpr (P == kInputGrad) {
                         mma_f16(tmem, desc128(quant + 2048 * i, 8192), desc128(dense + 32 * i, 0), p.idesc, acc);
                     } else {
-                        const uint64_t x = desc128(quant + 2048 * i, 8192);
-                        mma_f16(tmem, desc128(dense + 2048 * i, 8192), x, p.idesc, acc);
-                        mma_f16(tmem + 128, desc128(dense + 16384 + 2048 * i, 8192), x, p.idesc, acc);
+                        mma_f16(tmem, desc128(quant + 2048 * i, 8192), desc128(dense + 2048 * i, 8192), p.idesc, acc);
                     }
                 }
                 mma_commit(stage_free(stage));
@@ -373,7 +359,7 @@ __global__ void __launch_bounds__((TMA ? 11 : 14) * 32, 1) int4_mma_kernel(const
         }
     }
 
-    // ---- the result: warps 0..7 read the accumulator (a warp reaches 32 of the 128 lanes, warp & 3)
+    // ---- the result: warps 0..15 read the accumulator (a warp reaches 32 of the 128 lanes, warp & 3)
     const uint32_t quad = tmem + ((32u * (warp & 3u)) << 16);
     if (warp < kExpandWarps) {
         if (!mbar_wait(done, 0)) err = EP_DEC_TIMEOUT;
@@ -381,57 +367,60 @@ __global__ void __launch_bounds__((TMA ? 11 : 14) * 32, 1) int4_mma_kernel(const
     }
     float *joint = reinterpret_cast<float *>(smem);  // sums for the cluster, where the stages were
     if constexpr (P == kScaleGrad) {
-        // lane: feature o; 128 columns times the codes, summed over 32 inputs, then over the group
-        const uint32_t per = 128 / a.group, half = warp >> 2, f = 128 * half + 32 * (warp & 3u) + lane, o = a0 + f;
+        // lane: input k; a column (output feature) times the codes, summed over the warp's 32 inputs by
+        // exchanging halves (31 shuffles for 32 columns, after which lane l has column l's sum); then the
+        // warps of a group and the cluster's CTAs, in order
+        const uint32_t per = 128 / a.group, k = uint32_t(b0) + 32 * (warp & 3u) + lane, place = 4 * ((k & 7u) / 2) + 16 * (k & 1u);
         if (warp < kExpandWarps) {
-            float sum[4] = {};
+            for (uint32_t c = 64 * (warp >> 2); c < 64 * (warp >> 2) + 64; c += 32) {
+                uint32_t w[32];
 #pragma unroll
-            for (uint32_t i = 0; i < 4; ++i) {  // 32 inputs: 16 bytes of codes
-                uint4 w = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-                const uint32_t word = uint32_t(b0) / 8 + 4 * i;
-                if (o < a.n && word < a.words) w = __ldg(reinterpret_cast<const uint4 *>(a.codes + int64_t(o) * a.words + word));
-                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                for (uint32_t i = 0; i < 32; ++i) {
+                    const uint32_t o = a0 + c + i;
+                    w[i] = o < a.n && k / 8 < a.words ? __ldg(a.codes + int64_t(o) * a.words + k / 8) : 0x88888888u;
+                }
+                float v[32];
 #pragma unroll
                 for (uint32_t h = 0; h < 2; ++h) {
-                    uint32_t r[16];
-                    tmem_load16(r, quad + 128 * half + 32 * i + 16 * h);
+                    uint32_t d[16];
+                    tmem_load16(d, quad + c + 16 * h);
 #pragma unroll
-                    for (uint32_t e = 0; e < 16; ++e) {
-                        const uint32_t in = e & 7u, code = (ws[2 * h + e / 8] >> (4 * (in / 2) + 16 * (in & 1u))) & 15u;
-                        sum[i] = fmaf(__uint_as_float(r[e]), float(int(code) - 8), sum[i]);
+                    for (uint32_t i = 0; i < 16; ++i)
+                        v[16 * h + i] = __uint_as_float(d[i]) * float(int((w[16 * h + i] >> place) & 15u) - 8);
+                }
+#pragma unroll
+                for (uint32_t s = 16; s > 0; s >>= 1) {
+                    const bool up = lane & s;
+#pragma unroll
+                    for (uint32_t i = 0; i < s; ++i) {
+                        const float got = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + s], s);
+                        v[i] = (up ? v[i + s] : v[i]) + got;
                     }
                 }
+                joint[256 * (warp & 3u) + c + lane] = v[0];
             }
-            if (per < 4) sum[0] += sum[1], sum[2] += sum[3];
-            if (per == 2) sum[1] = sum[2];
-            if (per == 1) sum[0] += sum[2];
-            if (splits > 1) {
-#pragma unroll
-                for (uint32_t i = 0; i < 4; ++i) joint[4 * f + i] = sum[i];
-            } else if (o < a.n) {
-#pragma unroll
-                for (uint32_t i = 0; i < 4; ++i) {
-                    const uint32_t g = uint32_t(b0) / a.group + i;
-                    if (i < per && g < a.groups) a.out[int64_t(o) * a.groups + g] = Elem<T>::bits(sum[i]);
+        }
+        if (splits > 1)
+            cluster_sync();
+        else
+            __syncthreads();
+        for (uint32_t e = rank * blockDim.x + threadIdx.x; e < 256 * per; e += splits * blockDim.x) {
+            const uint32_t row = a0 + e / per, i = e % per, g = uint32_t(b0) / a.group + i;
+            float s = 0.0f;
+            for (uint32_t q = 0; q < splits; ++q)
+                for (uint32_t w = i * (4 / per); w < (i + 1) * (4 / per); ++w) {
+                    const float *at = &joint[256 * w + e / per];
+                    s += splits > 1 ? ld_cluster(at, q) : *at;
                 }
-            }
+            if (row < a.n && g < a.groups) a.out[int64_t(row) * a.groups + g] = Elem<T>::bits(s);
         }
-        if (splits > 1) {
-            cluster_sync();
-            for (uint32_t e = rank * blockDim.x + threadIdx.x; e < 256 * per; e += splits * blockDim.x) {
-                const uint32_t row = a0 + e / per, i = e % per, g = uint32_t(b0) / a.group + i;
-                float s = 0.0f;
-                for (uint32_t q = 0; q < splits; ++q) s += ld_cluster(&joint[4 * (e / per) + i], q);
-                if (row < a.n && g < a.groups) a.out[int64_t(row) * a.groups + g] = Elem<T>::bits(s);
-            }
-            cluster_sync();
-        }
+        if (splits > 1) cluster_sync();
     } else {
         const uint32_t J = P == kForward ? a.n : a.k;
         if (warp < kExpandWarps) {
             const uint32_t f = 32 * (warp & 3u) + lane, j = a0 + f;
             const float b = P == kForward && a.bias && j < J ? Elem<T>::f(__ldg(a.bias + j)) : 0.0f;
-            for (uint32_t c = 16 * (warp >> 2); c < p.bn; c += 32) {
+            for (uint32_t c = 16 * (warp >> 2); c < p.bn; c += 16 * kGroups) {
                 uint32_t r[16];
                 tmem_load16(r, quad + c);
                 if (splits > 1) {
@@ -529,7 +518,7 @@ int launch_mma(const Int4Args &a, int sms, cudaStream_t s) {
     p.raws = std::min<uint32_t>(kMaxRaws, uint32_t((kSmemMost - kBarBytes - p.stages * stage) / raw));
     const size_t bytes = size_t(p.stages) * stage + size_t(p.raws) * raw + kBarBytes;
     // accumulator fp32, A and B of T; the scale gradient's operands and the input gradient's weight MN-major
-    const uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u, n = P == kScaleGrad ? 128 : p.bn;
+    const uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u, n = P == kScaleGrad ? 256 : p.bn;
     p.idesc = (1u << 4) | (type << 7) | (type << 10) | (P != kForward ? 1u << 15 : 0u) | (P == kScaleGrad ? 1u << 16 : 0u) |
               ((n >> 3) << 17) | ((128u >> 4) << 24);
     p.tmem_cols = 32;
@@ -557,7 +546,7 @@ int launch_mma(const Int4Args &a, int sms, cudaStream_t s) {
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(tiles_a * tiles_b), splits);
-    cfg.blockDim = dim3((tma ? 11 : 14) * 32);
+    cfg.blockDim = dim3((kDenseWarp0 + (tma ? 1 : kLoadWarps)) * 32);
     cfg.dynamicSmemBytes = bytes;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
