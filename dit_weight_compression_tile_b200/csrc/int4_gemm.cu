@@ -13,42 +13,45 @@ namespace {
 
 enum Product { kForward, kInputGrad, kScaleGrad };
 
-// One CTA computes one tile of D = sum over a contraction in steps of 64:
+// Tiles of D = a sum over a contraction in steps of 64:
 //   forward         D[o, t]: 128 output features x bn tokens, contraction over the inputs k
 //   input gradient  D[k, t]: 128 inputs x bn tokens, contraction over the output features o
 //   scale gradient  D[k, o]: 128 inputs x 256 output features, contraction over the tokens t
-// Roles: warps 0..15 expand the quantized operand (weight codes, or checkpoint codes in the scale
-// gradient), warp 16 issues the matrix instructions, warp 17 copies the quantized operand's bytes, warp 18
-// the dense operand (x or dy) by TMA, or warps 18..21 through registers where it is not 16-byte aligned.  Rings in shared memory:
-//   raw    the quantized operand's bytes, by TMA, 16 KB slots of four steps (scale gradient: two)
+// One CTA per SM walks over tiles.  Roles: warps 0..15 expand the quantized operand (weight codes, or
+// checkpoint codes in the scale gradient), warps 16..19 turn finished accumulators into output, warp 20
+// issues the matrix instructions, warp 21 copies the quantized operand's bytes, warp 22 the dense operand
+// (x or dy) by TMA, or warps 22..25 through registers where it is not 16-byte aligned.
+// Rings in shared memory, running on over the tiles:
+//   raw    the quantized operand's bytes, by TMA, slots of four steps (scale gradient: one)
 //   stage  one step's operands: 16 KB expanded (16-bit), and the dense tile (bn or 4 x 64 rows of 128
 //          bytes), both rows of 64 elements with the 128-byte swizzle
 // The expanded operand's rows follow the stored codes (64 consecutive inputs of one output feature or
 // token), so the forward's W is K-major (rows o, 64 k), and the input gradient's W^T and the scale
 // gradient's x are MN-major (rows o or t, twice 64 k); dy is MN-major in the scale gradient (rows t, four
-// times 64 o).  The accumulator stays in tensor memory (bn or 256 columns).
+// times 64 o).  Two accumulators in tensor memory: one tile's is read out while the next one's is built.
 // Few tiles: the contraction is split over a cluster's CTAs, whose accumulators (scale gradient: group
 // sums) are joined through distributed shared memory, in rank order.
-constexpr uint32_t kGroups = 4, kExpandWarps = 4 * kGroups, kMmaWarp = kExpandWarps, kRawWarp = kMmaWarp + 1;
-constexpr uint32_t kDenseWarp0 = kRawWarp + 1, kLoadWarps = 4;
+constexpr uint32_t kGroups = 4, kExpandWarps = 4 * kGroups, kOutWarp0 = kExpandWarps, kOutWarps = 4;
+constexpr uint32_t kMmaWarp = kOutWarp0 + kOutWarps, kRawWarp = kMmaWarp + 1, kDenseWarp0 = kRawWarp + 1, kLoadWarps = 4;
 constexpr uint32_t kQuantBytes = 16384, kBarBytes = 512, kMaxStages = 8, kMaxRaws = 8;
 
 struct MmaArgs {
     CUtensorMap dense, raw;
     Int4Args a;
     uint32_t bn;        // tokens of a tile (scale gradient: 128 inputs)
-    uint32_t tiles_b;   // tiles along the second index of D
+    uint32_t tiles, tiles_b;  // of D, and of its second index
     uint32_t steps;     // of 64 along the contraction
     uint32_t slots;     // raw slots along the contraction
     uint32_t stages, raws, dense_bytes;
-    uint32_t idesc, tmem_cols;
+    uint32_t idesc, tmem_cols;  // tensor memory: two accumulators
     uint32_t dense_align;  // 4 or 2 bytes, where the dense operand is not copied by TMA
 };
 
 template <int P>
 struct Shape {
-    static constexpr uint32_t kSlotSteps = P == kScaleGrad ? 2 : 4;
-    static constexpr uint32_t kRawBytes = 16384;
+    static constexpr uint32_t kSlotSteps = P == kScaleGrad ? 1 : 4;
+    static constexpr uint32_t kRawBytes = P == kScaleGrad ? 8192 : 16384;
+    static constexpr uint32_t kJointBytes = P == kScaleGrad ? 2048 : 0;  // the output warps' sums
 };
 
 // shared-memory matrix descriptor, 128-byte swizzle: rows of 128 bytes, 8-row groups 1024 bytes apart.
@@ -68,8 +71,11 @@ __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void mbar_arrive(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void named_sync(uint32_t id, uint32_t threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 __device__ __forceinline__ void sts128(uint32_t a, const uint32_t (&v)[4]) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
@@ -117,28 +123,47 @@ struct Act<__half> {
     }
 };
 
+// A walk over the steps of a CTA's tiles, `n` steps a tile: tile `tile`, its step `i`
+struct Walk {
+    uint32_t tile, i;
+    __device__ __forceinline__ void advance(uint32_t by, uint32_t n) {
+        for (i += by; i >= n; i -= n) tile += gridDim.x;
+    }
+};
+// A place in a ring of `size` buffers and the parity of its turn
+struct Ring {
+    uint32_t at = 0, phase = 0;
+    __device__ __forceinline__ void advance(uint32_t by, uint32_t size) {
+        for (at += by; at >= size; at -= size) phase ^= 1u;
+    }
+};
+
 template <typename T, int P, bool TMA>
-__global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1) int4_mma_kernel(const __grid_constant__ MmaArgs p) {
+__global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1)
+    int4_mma_kernel(const __grid_constant__ MmaArgs p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr uint32_t kSlotSteps = Shape<P>::kSlotSteps, kRawBytes = Shape<P>::kRawBytes;
     const Int4Args &a = p.a;
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
     const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
     const uint32_t stage_bytes = kQuantBytes + p.dense_bytes;
-    const uint32_t raw0 = base + p.stages * stage_bytes, bars = raw0 + p.raws * kRawBytes;
+    const uint32_t raw0 = base + p.stages * stage_bytes, joint0 = raw0 + p.raws * kRawBytes;
+    const uint32_t bars = joint0 + Shape<P>::kJointBytes;
     auto quant_full = [&](uint32_t i) { return bars + 8 * i; };
     auto dense_full = [&](uint32_t i) { return bars + 64 + 8 * i; };
     auto stage_free = [&](uint32_t i) { return bars + 128 + 8 * i; };
     auto raw_full = [&](uint32_t i) { return bars + 192 + 8 * i; };
     auto raw_free = [&](uint32_t i) { return bars + 256 + 8 * i; };
-    const uint32_t done = bars + 320, tmem_slot = bars + 328;
-    // the tile, and this CTA's share of the contraction (whole raw slots)
-    const uint32_t ta = blockIdx.x / p.tiles_b, tb = blockIdx.x % p.tiles_b;
-    const uint32_t a0 = ta * (P == kScaleGrad ? 256 : 128);  // first o (forward, scale gradient) or k
-    const int64_t b0 = int64_t(tb) * p.bn;                   // first token, or k (scale gradient)
+    auto acc_full = [&](uint32_t i) { return bars + 320 + 8 * i; };
+    auto acc_free = [&](uint32_t i) { return bars + 336 + 8 * i; };
+    const uint32_t tmem_slot = bars + 352;
+    // this CTA's share of the contraction (whole raw slots); the tile's first o (forward) or k, and its
+    // first token or (scale gradient) o
     const uint32_t splits = gridDim.y, rank = blockIdx.y;
     const uint32_t slot_lo = uint32_t(uint64_t(rank) * p.slots / splits), slot_hi = uint32_t(uint64_t(rank + 1) * p.slots / splits);
-    const uint32_t step_lo = slot_lo * kSlotSteps, step_hi = min(slot_hi * kSlotSteps, p.steps);
+    const uint32_t step_lo = slot_lo * kSlotSteps, steps = min(slot_hi * kSlotSteps, p.steps) - step_lo;
+    auto first_a = [&](uint32_t tile) { return 128 * (tile / p.tiles_b); };
+    auto first_b = [&](uint32_t tile) { return int64_t(tile % p.tiles_b) * p.bn; };
 
     if (threadIdx.x == 0) {
         for (uint32_t i = 0; i < p.stages; ++i) {
@@ -148,9 +173,12 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
         }
         for (uint32_t i = 0; i < p.raws; ++i) {
             mbar_init(raw_full(i), 1);
-            mbar_init(raw_free(i), 4 * kSlotSteps);
+            mbar_init(raw_free(i), kExpandWarps);
         }
-        mbar_init(done, 1);
+        for (uint32_t i = 0; i < 2; ++i) {
+            mbar_init(acc_full(i), 1);
+            mbar_init(acc_free(i), kOutWarps);
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async();
     }
@@ -164,19 +192,23 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = lds32(tmem_slot);
     uint32_t err = 0;
+    // sums for the cluster lie where the stages were (one tile a CTA then), the scale gradient's otherwise
+    // in their own place
+    float *joint = reinterpret_cast<float *>(smem + (P == kScaleGrad && splits == 1 ? joint0 - base : 0u));
 
     if (warp < kExpandWarps) {
         // ---- expand the quantized operand: group warp / 4 takes every kGroups-th step, a row of 64 elements
         // (128 bytes) a thread: row r of the 128, that is (forward) output feature r, or (input gradient, scale
         // gradient) output feature or token r % 64, inputs 64 (r / 64) .. of the tile's 128
-        const uint32_t group = warp >> 2, r = 32 * (warp & 3u) + lane, cc = r >> 6, steps = step_hi - step_lo;
-        uint32_t stage = group, phase = 0;
+        const uint32_t group = warp >> 2, r = 32 * (warp & 3u) + lane, cc = r >> 6;
         uint32_t scale[2];
         // the thread's scales in a step (0 where there is none), read one step ahead
-        auto load_scales = [&](uint32_t step) {
+        auto load_scales = [&](const Walk &w) {
+            if (w.tile >= p.tiles) return;
+            const uint32_t a0 = first_a(w.tile), step = step_lo + w.i;
             if constexpr (P == kScaleGrad) {
                 const uint32_t t = 64 * step + (r & 63u);
-                scale[0] = t < a.m ? __float_as_uint(__ldg(a.act_scales + int64_t(t) * a.act_groups + tb)) : 0u;
+                scale[0] = t < a.m ? __float_as_uint(__ldg(a.act_scales + int64_t(t) * a.act_groups + a0 / 128)) : 0u;
             } else {
                 const uint32_t o = P == kForward ? a0 + r : 64 * step + (r & 63u);
                 const uint32_t k = P == kForward ? 64 * step : a0 + 64 * cc;
@@ -185,16 +217,31 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
                 scale[1] = o < a.n && k + 32 < a.k ? __ldg(row + (k + 32) / a.group) : 0u;
             }
         };
-        if (group < steps) load_scales(step_lo + group);
-        for (uint32_t n = group; n < steps; n += kGroups) {  // steps counted from this CTA's first
-            const uint32_t slot = n / kSlotSteps, js = n % kSlotSteps, raw = slot % p.raws;
-            const uint32_t now[2] = {scale[0], scale[1]};
-            if (n + kGroups < steps) load_scales(step_lo + n + kGroups);
-            if (!mbar_wait(raw_full(raw), (slot / p.raws) & 1u)) {
+        Walk mine{blockIdx.x, 0};  // this group's next step
+        mine.advance(group, steps);
+        Ring stage, raw;
+        stage.advance(group, p.stages);
+        load_scales(mine);
+        // every group passes every slot, in order, and frees it, whether it has a step there or not: none is
+        // ever further ahead of another than the ring is long, so no turn is taken for another
+        for (Walk at{blockIdx.x, 0}; at.tile < p.tiles; raw.advance(1, p.raws)) {
+            if (!mbar_wait(raw_full(raw.at), raw.phase)) {
                 err = EP_DEC_TIMEOUT;
                 break;
             }
-            const uint32_t src = raw0 + raw * kRawBytes;
+            const uint32_t left = min(kSlotSteps, steps - at.i), js = mine.i - at.i;
+            const bool has = mine.tile == at.tile && js < left;
+            at.i += left;
+            if (at.i == steps) at.i = 0, at.tile += gridDim.x;
+            if (!has) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(raw_free(raw.at), 1);
+                continue;
+            }
+            const uint32_t now[2] = {scale[0], scale[1]};
+            mine.advance(kGroups, steps);
+            load_scales(mine);
+            const uint32_t src = raw0 + raw.at * kRawBytes;
             uint32_t out[8][4];
             if constexpr (P == kScaleGrad) {
                 const float s = __uint_as_float(now[0]) * Act<T>::kScale;
@@ -204,249 +251,281 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
                 const uint32_t row = 64 * js + (r & 63u);
 #pragma unroll
                 for (uint32_t i = 0; i < 4; ++i) {
-                    uint32_t w[4];
-                    lds128(w, src + 128 * row + 16 * ((4 * cc + i) ^ (row & 7u)));
+                    uint32_t q[4];
+                    lds128(q, src + 128 * row + 16 * ((4 * cc + i) ^ (row & 7u)));
 #pragma unroll
                     for (uint32_t e = 0; e < 8; ++e) {
-                        const uint32_t v = Act<T>::pair(w[e / 2], e & 1u);
+                        const uint32_t v = Act<T>::pair(q[e / 2], e & 1u);
                         out[2 * i + e / 4][e & 3u] = Codes<T>::fma2(v, hi, mul2<T>(v, lo));
                     }
                 }
             } else {
 #pragma unroll
                 for (uint32_t i = 0; i < 2; ++i) {
-                    uint32_t w[4];
+                    uint32_t q[4];
                     if constexpr (P == kForward) {
-                        lds128(w, src + 128 * r + 16 * ((2 * js + i) ^ (r & 7u)));
+                        lds128(q, src + 128 * r + 16 * ((2 * js + i) ^ (r & 7u)));
                     } else {
                         const uint32_t row = 64 * js + (r & 63u);
-                        lds128(w, src + 64 * row + 16 * ((2 * cc + i) ^ ((row >> 1) & 3u)));
+                        lds128(q, src + 64 * row + 16 * ((2 * cc + i) ^ ((row >> 1) & 3u)));
                     }
                     const uint32_t s2 = now[i] | (now[i] << 16);
 #pragma unroll
                     for (uint32_t e = 0; e < 4; ++e) {
-                        code_pairs<T>(w[e], out[4 * i + e]);
+                        code_pairs<T>(q[e], out[4 * i + e]);
 #pragma unroll
                         for (uint32_t h = 0; h < 4; ++h) out[4 * i + e][h] = mul2<T>(out[4 * i + e][h], s2);
                     }
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(raw_free(raw));
-            if (!mbar_wait(stage_free(stage), phase ^ 1u)) {
+            if (lane == 0) mbar_arrive(raw_free(raw.at), 1);
+            if (!mbar_wait(stage_free(stage.at), stage.phase ^ 1u)) {
                 err = EP_DEC_TIMEOUT;
                 break;
             }
-            const uint32_t dst = base + stage * stage_bytes + 128 * r;
+            const uint32_t dst = base + stage.at * stage_bytes + 128 * r;
 #pragma unroll
             for (uint32_t i = 0; i < 8; ++i) sts128(dst + 16 * (i ^ (r & 7u)), out[i]);
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(quant_full(stage));
-            for (stage += kGroups; stage >= p.stages; stage -= p.stages) phase ^= 1u;
+            if (lane == 0) mbar_arrive(quant_full(stage.at), 1);
+            stage.advance(kGroups, p.stages);
         }
-    } else if (warp == kRawWarp) {
-        // ---- the quantized operand's bytes, a slot ahead of need as buffers come free
-        if (lane == 0) {
-            uint32_t raw = 0, phase = 0, copies = 0;
-            for (uint32_t slot = slot_lo; slot < slot_hi; ++slot, ++copies) {
-                if (!mbar_wait(raw_free(raw), phase ^ 1u)) {
+    } else if (warp < kMmaWarp) {
+        // ---- the output: warp q of the four reads lanes 32 q .. of the accumulator
+        const uint32_t q = warp - kOutWarp0;
+        Ring acc;
+        for (uint32_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x, acc.advance(1, 2)) {
+            const uint32_t a0 = first_a(tile);
+            const int64_t b0 = first_b(tile);
+            // after a lost wait the warps still meet at their barriers (and wait no more)
+            if (!err && !mbar_wait(acc_full(acc.at), acc.phase)) err = EP_DEC_TIMEOUT;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t from = tmem + ((32u * q) << 16) + acc.at * p.bn;
+            if constexpr (P == kScaleGrad) {
+                // lane: input k; a column (output feature) times the codes, summed over the warp's 32 inputs
+                // by exchanging halves (16 shuffles for 16 columns, after which lanes l and l + 16 have column
+                // l's sum); then the warps of a group and the cluster's CTAs, in order
+                const uint32_t k = a0 + 32 * q + lane, place = 4 * ((k & 7u) / 2) + 16 * (k & 1u), o0 = uint32_t(b0);
+                const uint32_t *codes = a.codes + k / 8;
+                uint32_t w[16];
+                auto load_codes = [&](uint32_t c) {
+#pragma unroll
+                    for (uint32_t i = 0; i < 16; ++i)
+                        w[i] = o0 + c + i < a.n && k / 8 < a.words ? __ldg(codes + int64_t(o0 + c + i) * a.words) : 0x88888888u;
+                };
+                load_codes(0);
+                for (uint32_t c = 0; c < 256; c += 16) {
+                    uint32_t d[16];
+                    tmem_load16(d, from + c);
+                    float v[16];
+#pragma unroll
+                    for (uint32_t i = 0; i < 16; ++i) v[i] = __uint_as_float(d[i]) * float(int((w[i] >> place) & 15u) - 8);
+                    if (c + 16 < 256) load_codes(c + 16);
+#pragma unroll
+                    for (uint32_t s = 8; s > 0; s >>= 1) {
+                        const bool up = lane & s;
+#pragma unroll
+                        for (uint32_t i = 0; i < s; ++i) {
+                            const float got = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + s], s);
+                            v[i] = (up ? v[i + s] : v[i]) + got;
+                        }
+                    }
+                    v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
+                    if (splits > 1) {
+                        if (lane < 16) joint[256 * q + c + lane] = v[0];
+                        continue;
+                    }
+                    if (lane < 16) joint[128 * q + (c & 127u) + lane] = v[0];
+                    if ((c & 127u) != 112) continue;
+                    named_sync(1, 32 * kOutWarps);
+                    const uint32_t per = 128 / a.group, span = 4 / per;
+                    for (uint32_t e = 32 * q + lane; e < 128 * per; e += 32 * kOutWarps) {
+                        const uint32_t row = o0 + c - 112 + e / per, i = e % per, g = a0 / a.group + i;
+                        float s = 0.0f;
+                        for (uint32_t h = i * span; h < (i + 1) * span; ++h) s += joint[128 * h + e / per];
+                        if (row < a.n && g < a.groups) a.out[int64_t(row) * a.groups + g] = Elem<T>::bits(s);
+                    }
+                    named_sync(1, 32 * kOutWarps);  // the sums are read before the next ones
+                }
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(acc_free(acc.at), 1);
+            } else {
+                const uint32_t J = P == kForward ? a.n : a.k, f = 32 * q + lane, j = a0 + f;
+                const float b = P == kForward && a.bias && j < J ? Elem<T>::f(__ldg(a.bias + j)) : 0.0f;
+                for (uint32_t c = 0; c < p.bn; c += 16) {
+                    uint32_t d[16];
+                    tmem_load16(d, from + c);
+                    if (splits > 1) {
+#pragma unroll
+                        for (uint32_t i = 0; i < 16; ++i) joint[128 * (c + i) + f] = __uint_as_float(d[i]);
+                    } else if (j < J) {
+#pragma unroll
+                        for (uint32_t i = 0; i < 16; ++i)
+                            if (b0 + c + i < a.m)
+                                a.out[(b0 + c + i) * J + j] = Elem<T>::bits(__uint_as_float(d[i]) * Codes<T>::kUnit + b);
+                    }
+                }
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(acc_free(acc.at), 1);
+            }
+        }
+    } else if (warp == kMmaWarp) {
+        // ---- the matrix instructions, 16 of the contraction each
+        Ring stage, acc;
+        for (uint32_t tile = blockIdx.x; tile < p.tiles && !err; tile += gridDim.x, acc.advance(1, 2)) {
+            if (!mbar_wait(acc_free(acc.at), acc.phase ^ 1u)) {
+                err = EP_DEC_TIMEOUT;
+                break;
+            }
+            for (uint32_t i = 0; i < steps; ++i) {
+                if (!mbar_wait(quant_full(stage.at), stage.phase) || !mbar_wait(dense_full(stage.at), stage.phase)) {
                     err = EP_DEC_TIMEOUT;
                     break;
                 }
-                mbar_expect(raw_full(raw), kRawBytes);
-                if constexpr (P == kForward)
-                    tma_load(raw0 + raw * kRawBytes, &p.raw, 128 * slot, a0, raw_full(raw));
-                else if constexpr (P == kInputGrad)
-                    tma_load(raw0 + raw * kRawBytes, &p.raw, a0 / 2, 256 * slot, raw_full(raw));
-                else
-                    tma_load(raw0 + raw * kRawBytes, &p.raw, uint32_t(b0), 128 * slot, raw_full(raw));
-                if (++raw == p.raws) raw = 0, phase ^= 1u;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                if (lane == 0) {
+                    const uint32_t quant = base + stage.at * stage_bytes, dense = quant + kQuantBytes, d = tmem + acc.at * p.bn;
+#pragma unroll
+                    for (uint32_t h = 0; h < 4; ++h) {
+                        const uint32_t more = i > 0 || h > 0;
+                        const uint64_t da = P == kForward ? desc128(quant + 32 * h, 0) : desc128(quant + 2048 * h, 8192);
+                        const uint64_t db = P == kScaleGrad ? desc128(dense + 2048 * h, 8192) : desc128(dense + 32 * h, 0);
+                        mma_f16(d, da, db, p.idesc, more);
+                    }
+                    mma_commit(stage_free(stage.at));
+                }
+                __syncwarp();
+                stage.advance(1, p.stages);
+            }
+            if (lane == 0) mma_commit(acc_full(acc.at));
+            __syncwarp();
+        }
+    } else if (warp == kRawWarp) {
+        // ---- the quantized operand's bytes, as buffers come free
+        if (lane == 0) {
+            Ring raw;
+            uint32_t copies = 0;
+            for (uint32_t tile = blockIdx.x; tile < p.tiles && !err; tile += gridDim.x) {
+                const uint32_t a0 = first_a(tile);
+                for (uint32_t slot = slot_lo; slot < slot_hi; ++slot, ++copies, raw.advance(1, p.raws)) {
+                    if (!mbar_wait(raw_free(raw.at), raw.phase ^ 1u)) {
+                        err = EP_DEC_TIMEOUT;
+                        break;
+                    }
+                    const uint32_t dst = raw0 + raw.at * kRawBytes, bar = raw_full(raw.at);
+                    mbar_expect(bar, kRawBytes);
+                    if constexpr (P == kForward)
+                        tma_load(dst, &p.raw, 128 * slot, a0, bar);
+                    else if constexpr (P == kInputGrad)
+                        tma_load(dst, &p.raw, a0 / 2, 256 * slot, bar);
+                    else
+                        tma_load(dst, &p.raw, a0, 64 * slot, bar);
+                }
             }
             // no copy is in flight when the CTA ends: the last use of each buffer
             for (uint32_t i = copies > p.raws ? copies - p.raws : 0; i < copies; ++i)
                 if (!mbar_wait(raw_full(i % p.raws), (i / p.raws) & 1u)) err = EP_DEC_TIMEOUT;
         }
         __syncwarp();
-    } else if (TMA && warp == kDenseWarp0) {
+    } else if (TMA) {
         // ---- the dense operand by TMA
         if (lane == 0) {
-            uint32_t stage = 0, phase = 0, copies = 0;
-            for (uint32_t step = step_lo; step < step_hi; ++step, ++copies) {
-                if (!mbar_wait(stage_free(stage), phase ^ 1u)) {
-                    err = EP_DEC_TIMEOUT;
-                    break;
-                }
-                const uint32_t dst = base + stage * stage_bytes + kQuantBytes;
-                mbar_expect(dense_full(stage), p.dense_bytes);
-                if constexpr (P == kScaleGrad) {
+            Ring stage;
+            uint32_t copies = 0;
+            for (uint32_t tile = blockIdx.x; tile < p.tiles && !err; tile += gridDim.x) {
+                const uint32_t b0 = uint32_t(first_b(tile));
+                for (uint32_t i = 0; i < steps; ++i, ++copies, stage.advance(1, p.stages)) {
+                    if (!mbar_wait(stage_free(stage.at), stage.phase ^ 1u)) {
+                        err = EP_DEC_TIMEOUT;
+                        break;
+                    }
+                    const uint32_t dst = base + stage.at * stage_bytes + kQuantBytes, bar = dense_full(stage.at);
+                    const uint32_t c = 64 * (step_lo + i);
+                    mbar_expect(bar, p.dense_bytes);
+                    if constexpr (P == kScaleGrad) {
 #pragma unroll
-                    for (uint32_t i = 0; i < 4; ++i) tma_load(dst + 8192 * i, &p.dense, a0 + 64 * i, 64 * step, dense_full(stage));
-                } else {
-                    tma_load(dst, &p.dense, 64 * step, uint32_t(b0), dense_full(stage));
+                        for (uint32_t h = 0; h < 4; ++h) tma_load(dst + 8192 * h, &p.dense, b0 + 64 * h, c, bar);
+                    } else {
+                        tma_load(dst, &p.dense, c, b0, bar);
+                    }
                 }
-                if (++stage == p.stages) stage = 0, phase ^= 1u;
             }
             for (uint32_t i = copies > p.stages ? copies - p.stages : 0; i < copies; ++i)
                 if (!mbar_wait(dense_full(i % p.stages), (i / p.stages) & 1u)) err = EP_DEC_TIMEOUT;
         }
         __syncwarp();
-    } else if (warp == kMmaWarp) {
-        // ---- the matrix instructions, 16 of the contraction each
-        uint32_t stage = 0, phase = 0;
-        for (uint32_t step = step_lo; step < step_hi; ++step) {
-            if (!mbar_wait(quant_full(stage), phase) || !mbar_wait(dense_full(stage), phase)) {
-                err = EP_DEC_TIMEOUT;
-                break;
-            }
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            if (lane == 0) {
-                const uint32_t quant = base + stage * stage_bytes, dense = quant + kQuantBytes;
-#pragma unroll
-                for (uint32_t i = 0; i < 4; ++i) {
-                    const uint32_t acc = step > step_lo || i > 0;
-                    if constexpr (P == kForward) {
-                        mma_f16(tmem, desc128(quant + 32 * i, 0), desc128(dense + 32 * i, 0), p.idesc, acc);
-                    } else if constexpr (P == kInputGrad) {
-                        mma_f16(tmem, desc128(quant + 2048 * i, 8192), desc128(dense + 32 * i, 0), p.idesc, acc);
-                    } else {
-                        mma_f16(tmem, desc128(quant + 2048 * i, 8192), desc128(dense + 2048 * i, 8192), p.idesc, acc);
-                    }
-                }
-                mma_commit(stage_free(stage));
-            }
-            __syncwarp();
-            if (++stage == p.stages) stage = 0, phase ^= 1u;
-        }
-        if (lane == 0) mma_commit(done);
-        __syncwarp();
-    } else if (!TMA && warp >= kDenseWarp0) {
+    } else {
         // ---- the dense operand through registers: 16-byte chunks of 8 elements, each checked
         const uint32_t rows = P == kScaleGrad ? 64 : p.bn, boxes = P == kScaleGrad ? 4 : 1;
         const uint32_t cols_all = P == kForward ? a.k : a.n;
-        uint32_t stage = 0, phase = 0;
-        for (uint32_t step = step_lo; step < step_hi; ++step) {
-            if (!mbar_wait(stage_free(stage), phase ^ 1u)) {
-                err = EP_DEC_TIMEOUT;
-                break;
-            }
-            const uint32_t dst = base + stage * stage_bytes + kQuantBytes;
-            for (uint32_t e = threadIdx.x - 32 * kDenseWarp0; e < boxes * rows * 8; e += 32 * kLoadWarps) {
-                const uint32_t c = e & 7u, r = (e >> 3) % rows, box = (e >> 3) / rows;
-                const int64_t t = (P == kScaleGrad ? 64 * int64_t(step) : b0) + r;
-                const uint32_t col = (P == kScaleGrad ? a0 + 64 * box : 64 * step) + 8 * c;
-                uint32_t v[4] = {0u, 0u, 0u, 0u};
-                if (t < a.m && col < cols_all) {
-                    const uint16_t *src = a.x + t * a.ldx + col;
-                    if (p.dense_align >= 4 && col + 8 <= cols_all) {
+        Ring stage;
+        for (uint32_t tile = blockIdx.x; tile < p.tiles && !err; tile += gridDim.x) {
+            const int64_t b0 = first_b(tile);
+            for (uint32_t i = 0; i < steps; ++i, stage.advance(1, p.stages)) {
+                const uint32_t step = step_lo + i;
+                if (!mbar_wait(stage_free(stage.at), stage.phase ^ 1u)) {
+                    err = EP_DEC_TIMEOUT;
+                    break;
+                }
+                const uint32_t dst = base + stage.at * stage_bytes + kQuantBytes;
+                for (uint32_t e = threadIdx.x - 32 * kDenseWarp0; e < boxes * rows * 8; e += 32 * kLoadWarps) {
+                    const uint32_t c = e & 7u, r = (e >> 3) % rows, box = (e >> 3) / rows;
+                    const int64_t t = (P == kScaleGrad ? 64 * int64_t(step) : b0) + r;
+                    const uint32_t col = (P == kScaleGrad ? uint32_t(b0) + 64 * box : 64 * step) + 8 * c;
+                    uint32_t v[4] = {0u, 0u, 0u, 0u};
+                    if (t < a.m && col < cols_all) {
+                        const uint16_t *src = a.x + t * a.ldx + col;
+                        if (p.dense_align >= 4 && col + 8 <= cols_all) {
 #pragma unroll
-                        for (uint32_t i = 0; i < 4; ++i) v[i] = __ldg(reinterpret_cast<const uint32_t *>(src) + i);
-                    } else {
+                            for (uint32_t h = 0; h < 4; ++h) v[h] = __ldg(reinterpret_cast<const uint32_t *>(src) + h);
+                        } else {
 #pragma unroll
-                        for (uint32_t i = 0; i < 4; ++i) {
-                            const uint32_t lo = col + 2 * i < cols_all ? __ldg(src + 2 * i) : 0u;
-                            const uint32_t hi = col + 2 * i + 1 < cols_all ? __ldg(src + 2 * i + 1) : 0u;
-                            v[i] = lo | (hi << 16);
+                            for (uint32_t h = 0; h < 4; ++h) {
+                                const uint32_t lo = col + 2 * h < cols_all ? __ldg(src + 2 * h) : 0u;
+                                const uint32_t hi = col + 2 * h + 1 < cols_all ? __ldg(src + 2 * h + 1) : 0u;
+                                v[h] = lo | (hi << 16);
+                            }
                         }
                     }
+                    sts128(dst + 8192 * box + 128 * r + 16 * (c ^ (r & 7u)), v);
                 }
-                sts128(dst + 8192 * box + 128 * r + 16 * (c ^ (r & 7u)), v);
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(dense_full(stage.at), 1);
             }
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(dense_full(stage));
-            if (++stage == p.stages) stage = 0, phase ^= 1u;
         }
     }
 
-    // ---- the result: warps 0..15 read the accumulator (a warp reaches 32 of the 128 lanes, warp & 3)
-    const uint32_t quad = tmem + ((32u * (warp & 3u)) << 16);
-    if (warp < kExpandWarps) {
-        if (!mbar_wait(done, 0)) err = EP_DEC_TIMEOUT;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    }
-    float *joint = reinterpret_cast<float *>(smem);  // sums for the cluster, where the stages were
-    if constexpr (P == kScaleGrad) {
-        // lane: input k; a column (output feature) times the codes, summed over the warp's 32 inputs by
-        // exchanging halves (31 shuffles for 32 columns, after which lane l has column l's sum); then the
-        // warps of a group and the cluster's CTAs, in order
-        const uint32_t per = 128 / a.group, k = uint32_t(b0) + 32 * (warp & 3u) + lane, place = 4 * ((k & 7u) / 2) + 16 * (k & 1u);
-        if (warp < kExpandWarps) {
-            for (uint32_t c = 64 * (warp >> 2); c < 64 * (warp >> 2) + 64; c += 32) {
-                uint32_t w[32];
-#pragma unroll
-                for (uint32_t i = 0; i < 32; ++i) {
-                    const uint32_t o = a0 + c + i;
-                    w[i] = o < a.n && k / 8 < a.words ? __ldg(a.codes + int64_t(o) * a.words + k / 8) : 0x88888888u;
-                }
-                float v[32];
-#pragma unroll
-                for (uint32_t h = 0; h < 2; ++h) {
-                    uint32_t d[16];
-                    tmem_load16(d, quad + c + 16 * h);
-#pragma unroll
-                    for (uint32_t i = 0; i < 16; ++i)
-                        v[16 * h + i] = __uint_as_float(d[i]) * float(int((w[16 * h + i] >> place) & 15u) - 8);
-                }
-#pragma unroll
-                for (uint32_t s = 16; s > 0; s >>= 1) {
-                    const bool up = lane & s;
-#pragma unroll
-                    for (uint32_t i = 0; i < s; ++i) {
-                        const float got = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + s], s);
-                        v[i] = (up ? v[i + s] : v[i]) + got;
-                    }
-                }
-                joint[256 * (warp & 3u) + c + lane] = v[0];
+    // ---- a split contraction: each CTA adds its share of the tile over the cluster
+    if (splits > 1) {
+        const uint32_t a0 = first_a(blockIdx.x);
+        const int64_t b0 = first_b(blockIdx.x);
+        cluster_sync();
+        if constexpr (P == kScaleGrad) {
+            const uint32_t per = 128 / a.group, span = 4 / per, o0 = uint32_t(b0);
+            for (uint32_t e = rank * blockDim.x + threadIdx.x; e < 256 * per; e += splits * blockDim.x) {
+                const uint32_t row = o0 + e / per, i = e % per, g = a0 / a.group + i;
+                float s = 0.0f;
+                for (uint32_t c = 0; c < splits; ++c)
+                    for (uint32_t h = i * span; h < (i + 1) * span; ++h) s += ld_cluster(&joint[256 * h + e / per], c);
+                if (row < a.n && g < a.groups) a.out[int64_t(row) * a.groups + g] = Elem<T>::bits(s);
             }
-        }
-        if (splits > 1)
-            cluster_sync();
-        else
-            __syncthreads();
-        for (uint32_t e = rank * blockDim.x + threadIdx.x; e < 256 * per; e += splits * blockDim.x) {
-            const uint32_t row = a0 + e / per, i = e % per, g = uint32_t(b0) / a.group + i;
-            float s = 0.0f;
-            for (uint32_t q = 0; q < splits; ++q)
-                for (uint32_t w = i * (4 / per); w < (i + 1) * (4 / per); ++w) {
-                    const float *at = &joint[256 * w + e / per];
-                    s += splits > 1 ? ld_cluster(at, q) : *at;
-                }
-            if (row < a.n && g < a.groups) a.out[int64_t(row) * a.groups + g] = Elem<T>::bits(s);
-        }
-        if (splits > 1) cluster_sync();
-    } else {
-        const uint32_t J = P == kForward ? a.n : a.k;
-        if (warp < kExpandWarps) {
-            const uint32_t f = 32 * (warp & 3u) + lane, j = a0 + f;
-            const float b = P == kForward && a.bias && j < J ? Elem<T>::f(__ldg(a.bias + j)) : 0.0f;
-            for (uint32_t c = 16 * (warp >> 2); c < p.bn; c += 16 * kGroups) {
-                uint32_t r[16];
-                tmem_load16(r, quad + c);
-                if (splits > 1) {
-#pragma unroll
-                    for (uint32_t i = 0; i < 16; ++i) joint[128 * (c + i) + f] = __uint_as_float(r[i]);
-                } else if (j < J) {
-#pragma unroll
-                    for (uint32_t i = 0; i < 16; ++i)
-                        if (b0 + c + i < a.m)
-                            a.out[(b0 + c + i) * J + j] = Elem<T>::bits(__uint_as_float(r[i]) * Codes<T>::kUnit + b);
-                }
-            }
-        }
-        if (splits > 1) {
-            cluster_sync();
-            const uint32_t f = threadIdx.x & 127u, j = a0 + f, rows = blockDim.x / 128;
+        } else {
+            const uint32_t J = P == kForward ? a.n : a.k, f = threadIdx.x & 127u, j = a0 + f, rows = blockDim.x / 128;
             if (threadIdx.x / 128 < rows && j < J) {
                 const float b = P == kForward && a.bias ? Elem<T>::f(__ldg(a.bias + j)) : 0.0f;
                 for (uint32_t c = rank * rows + threadIdx.x / 128; c < p.bn && b0 + c < a.m; c += splits * rows) {
                     float s = 0.0f;
-                    for (uint32_t q = 0; q < splits; ++q) s += ld_cluster(&joint[128 * c + f], q);
+                    for (uint32_t h = 0; h < splits; ++h) s += ld_cluster(&joint[128 * c + f], h);
                     a.out[(b0 + c) * J + j] = Elem<T>::bits(s * Codes<T>::kUnit + b);
                 }
             }
-            cluster_sync();
         }
+        cluster_sync();
     }
     if (err && a.status && lane == 0) atomicOr(a.status, err);
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -496,33 +575,34 @@ int launch_mma(const Int4Args &a, int sms, cudaStream_t s) {
     p.steps = uint32_t((contraction + 63) / 64);
     p.slots = (p.steps + Shape<P>::kSlotSteps - 1) / Shape<P>::kSlotSteps;
     uint64_t tiles_a, tiles_b;
+    tiles_a = ((P == kForward ? a.n : a.k) + 127) / 128;
     if (P == kScaleGrad) {
-        p.bn = 128;
-        tiles_a = (a.n + 255) / 256;
-        tiles_b = (a.k + 127) / 128;
-        p.dense_bytes = 32768;
+        p.bn = 256;
+        tiles_b = (a.n + 255) / 256;
     } else {
-        tiles_a = ((P == kForward ? a.n : a.k) + 127) / 128;
         tiles_b = uint64_t(a.m + 255) / 256;
         p.bn = uint32_t(((a.m + int64_t(tiles_b) - 1) / int64_t(tiles_b) + 15) / 16 * 16);
-        p.dense_bytes = p.bn * 128;
     }
+    p.dense_bytes = p.bn * 128;
     if (tiles_a * tiles_b > 0x7fffffff) return EP_ERR_UNSUPPORTED;
+    p.tiles = uint32_t(tiles_a * tiles_b);
     p.tiles_b = uint32_t(tiles_b);
     uint32_t splits = 1;
-    if (tiles_a * tiles_b < uint64_t(sms))
-        splits = std::max(1u, std::min({8u, uint32_t(sms / (tiles_a * tiles_b)), p.slots / (P == kScaleGrad ? 2u : 1u)}));
-    const uint32_t stage = kQuantBytes + p.dense_bytes, raw = Shape<P>::kRawBytes;
-    p.raws = 2;
-    p.stages = std::min<uint32_t>(kMaxStages, uint32_t((kSmemMost - kBarBytes - p.raws * raw) / stage));
-    p.raws = std::min<uint32_t>(kMaxRaws, uint32_t((kSmemMost - kBarBytes - p.stages * stage) / raw));
-    const size_t bytes = size_t(p.stages) * stage + size_t(p.raws) * raw + kBarBytes;
+    if (p.tiles < uint32_t(sms)) splits = std::max(1u, std::min({8u, sms / p.tiles, p.slots / (P == kScaleGrad ? 4u : 1u)}));
+    const uint32_t stage = kQuantBytes + p.dense_bytes, raw = Shape<P>::kRawBytes, fixed = kBarBytes + Shape<P>::kJointBytes;
+    p.raws = P == kScaleGrad ? 4 : 2;
+    p.stages = std::min<uint32_t>(kMaxStages, uint32_t((kSmemMost - fixed - p.raws * raw) / stage));
+    p.raws = std::min<uint32_t>(kMaxRaws, uint32_t((kSmemMost - fixed - p.stages * stage) / raw));
+    // a group waits for the matrix instructions that read its stage last; it has seen those of the turn
+    // before done only if the ring holds a step of every group
+    if (p.stages < kGroups) return EP_ERR_UNSUPPORTED;
+    const size_t bytes = size_t(p.stages) * stage + size_t(p.raws) * raw + fixed;
     // accumulator fp32, A and B of T; the scale gradient's operands and the input gradient's weight MN-major
-    const uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u, n = P == kScaleGrad ? 256 : p.bn;
+    const uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
     p.idesc = (1u << 4) | (type << 7) | (type << 10) | (P != kForward ? 1u << 15 : 0u) | (P == kScaleGrad ? 1u << 16 : 0u) |
-              ((n >> 3) << 17) | ((128u >> 4) << 24);
+              ((p.bn >> 3) << 17) | ((128u >> 4) << 24);
     p.tmem_cols = 32;
-    while (p.tmem_cols < (P == kScaleGrad ? 256 : p.bn)) p.tmem_cols *= 2;
+    while (p.tmem_cols < 2 * p.bn) p.tmem_cols *= 2;
     const uint64_t dense_cols = P == kForward ? a.k : a.n;
     const int64_t ld = a.m > 1 ? a.ldx : int64_t((dense_cols + 7) / 8 * 8);
     const bool tma = !misaligned(a.x, 16) && ld % 8 == 0 && ld < (int64_t(1) << 38) && a.m <= 0x7fffffff;
@@ -531,7 +611,7 @@ int launch_mma(const Int4Args &a, int sms, cudaStream_t s) {
     const uint64_t pitch = P == kScaleGrad ? uint64_t(act8_row_bytes(a.k)) : uint64_t(a.words) * 4;
     const void *quant = P == kScaleGrad ? static_cast<const void *>(a.act) : static_cast<const void *>(a.codes);
     if (!tensor_map(&p.raw, quant, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, pitch, P == kScaleGrad ? uint64_t(a.m) : a.n, pitch,
-                    P == kInputGrad ? 64 : 128, P == kInputGrad ? 256 : 128))
+                    P == kInputGrad ? 64 : 128, P == kForward ? 128 : P == kInputGrad ? 256 : 64))
         return EP_ERR_CUDA;
     if (tma && !tensor_map(&p.dense, a.x, dt, 2, dense_cols, uint64_t(a.m), uint64_t(ld) * 2, 64, P == kScaleGrad ? 64 : p.bn))
         return EP_ERR_CUDA;
@@ -545,7 +625,7 @@ int launch_mma(const Int4Args &a, int sms, cudaStream_t s) {
         allowed[tma].fetch_or(uint64_t(1) << device);
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(tiles_a * tiles_b), splits);
+    cfg.gridDim = dim3(splits > 1 ? p.tiles : std::min(p.tiles, uint32_t(sms)), splits);
     cfg.blockDim = dim3((kDenseWarp0 + (tma ? 1 : kLoadWarps)) * 32);
     cfg.dynamicSmemBytes = bytes;
     cfg.stream = s;
