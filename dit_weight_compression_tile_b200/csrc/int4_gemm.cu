@@ -16,29 +16,36 @@ enum Product { kForward, kInputGrad, kScaleGrad };
 // Tiles of D = a sum over a contraction in steps of 64:
 //   forward         D[o, t]: 128 output features x bn tokens, contraction over the inputs k
 //   input gradient  D[k, t]: 128 inputs x bn tokens, contraction over the output features o
-//   scale gradient  D[k, o]: 128 inputs x 256 output features, contraction over the tokens t
-// One CTA per SM walks over tiles.  Roles: warps 0..15 expand the quantized operand (weight codes, or
-// checkpoint codes in the scale gradient), warps 16..19 turn finished accumulators into output, warp 20
-// issues the matrix instructions, warp 21 copies the quantized operand's bytes, warp 22 the dense operand
-// (x or dy) by TMA, or warps 22..25 through registers where it is not 16-byte aligned.
+//   scale gradient  D[o, k]: 128 output features x 128 inputs, contraction over the tokens t
+// One CTA per SM walks over tiles.  In the PAIR form two CTAs of a cluster share a tile twice as wide
+// (cta_group::2): each expands 128 rows of the quantized operand and copies half of the dense one (forward and
+// input gradient: its 128 features against all bn tokens; scale gradient: its 128 output features
+// against all 256 inputs), so that an SM's shared memory carries 32 KB a step instead of 48: its
+// bandwidth, taken by the copies in, the expanded stores and the matrix unit's reads, is what bounds the
+// single form (2048 x 8192 x 8192: single 250 us).
+// Roles: warps 0..15 expand the quantized operand (weight codes, or checkpoint codes in the scale gradient),
+// warps 16..19 turn finished accumulators into output, warp 20 issues the matrix instructions (PAIR: the
+// first CTA's, for both), warp 21 copies the quantized operand's bytes, warp 22 the dense operand (x or
+// dy) by TMA, or warps 22..25 through registers where it is not 16-byte aligned.
 // Rings in shared memory, running on over the tiles:
 //   raw    the quantized operand's bytes, by TMA, slots of four steps (scale gradient: one)
-//   stage  one step's operands: 16 KB expanded (16-bit), and the dense tile (bn or 4 x 64 rows of 128
-//          bytes), both rows of 64 elements with the 128-byte swizzle
+//   stage  one step's operands: 16 KB expanded (16-bit), and the dense tile (up to 256 or, scale gradient,
+//          twice 64 rows of 128 bytes), both rows of 64 elements with the 128-byte swizzle
 // The expanded operand's rows follow the stored codes (64 consecutive inputs of one output feature or
 // token), so the forward's W is K-major (rows o, 64 k), and the input gradient's W^T and the scale
-// gradient's x are MN-major (rows o or t, twice 64 k); dy is MN-major in the scale gradient (rows t, four
-// times 64 o).  Two accumulators in tensor memory: one tile's is read out while the next one's is built.
+// gradient's x are MN-major (rows o or t, twice 64 k); dy is MN-major in the scale gradient (rows t, twice
+// 64 o).  Two accumulators in tensor memory: one tile's is read out while the next one's is built.
 // Few tiles: the contraction is split over a cluster's CTAs, whose accumulators (scale gradient: group
 // sums) are joined through distributed shared memory, in rank order.
 constexpr uint32_t kGroups = 4, kExpandWarps = 4 * kGroups, kOutWarp0 = kExpandWarps, kOutWarps = 4;
 constexpr uint32_t kMmaWarp = kOutWarp0 + kOutWarps, kRawWarp = kMmaWarp + 1, kDenseWarp0 = kRawWarp + 1, kLoadWarps = 4;
 constexpr uint32_t kQuantBytes = 16384, kBarBytes = 512, kMaxStages = 8, kMaxRaws = 8;
+constexpr uint32_t kPairMask = 3;  // both CTAs of a pair
 
 struct MmaArgs {
     CUtensorMap dense, raw;
     Int4Args a;
-    uint32_t bn;        // tokens of a tile (scale gradient: 128 inputs)
+    uint32_t bn;        // columns of an accumulator: tokens, or inputs (scale gradient)
     uint32_t tiles, tiles_b;  // of D, and of its second index
     uint32_t steps;     // of 64 along the contraction
     uint32_t slots;     // raw slots along the contraction
@@ -51,7 +58,6 @@ template <int P>
 struct Shape {
     static constexpr uint32_t kSlotSteps = P == kScaleGrad ? 1 : 4;
     static constexpr uint32_t kRawBytes = P == kScaleGrad ? 8192 : 16384;
-    static constexpr uint32_t kJointBytes = P == kScaleGrad ? 2048 : 0;  // the output warps' sums
 };
 
 // shared-memory matrix descriptor, 128-byte swizzle: rows of 128 bytes, 8-row groups 1024 bytes apart.
@@ -61,21 +67,72 @@ __device__ __forceinline__ uint64_t desc128(uint32_t addr, uint32_t lead) {
     return uint64_t((addr >> 4) & 0x3fffu) | (uint64_t((lead >> 4) & 0x3fffu) << 16) | (uint64_t(1024 >> 4) << 32) |
            (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
+template <bool PAIR>
 __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
 }
+// an arrival when the matrix instructions before it are done, on the barrier of this CTA, or of both
+template <bool PAIR>
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    if constexpr (PAIR)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+            "h"(uint16_t(kPairMask))
+            : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void mbar_arrive(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void named_sync(uint32_t id, uint32_t threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+// the address of a place of this CTA's shared memory in the pair's first CTA
+__device__ __forceinline__ uint32_t in_first(uint32_t addr) {
+    uint32_t there;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(there) : "r"(addr));
+    return there;
+}
+// an arrival on the barrier of the CTA whose warp 20 issues the matrix instructions
+template <bool PAIR>
+__device__ __forceinline__ void arrive_issuer(uint32_t bar) {
+    if constexpr (PAIR)
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_first(bar)) : "memory");
+    else
+        mbar_arrive(bar);
+}
+// mbar_wait for a barrier that the other CTA arrives on
+template <bool PAIR>
+__device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity) {
+    if constexpr (!PAIR) return mbar_wait(bar, parity);
+    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, "
+            "p;\n}\n"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return true;
+    }
+    return false;
+}
+// a box into this CTA's shared memory that completes on a barrier of the pair's first CTA
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap *map, uint32_t col, uint32_t row, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(dst),
+        "l"(map), "r"(col), "r"(row), "r"(in_first(bar))
+        : "memory");
 }
 __device__ __forceinline__ void sts128(uint32_t a, const uint32_t (&v)[4]) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
@@ -126,8 +183,8 @@ struct Act<__half> {
 // A walk over the steps of a CTA's tiles, `n` steps a tile: tile `tile`, its step `i`
 struct Walk {
     uint32_t tile, i;
-    __device__ __forceinline__ void advance(uint32_t by, uint32_t n) {
-        for (i += by; i >= n; i -= n) tile += gridDim.x;
+    __device__ __forceinline__ void advance(uint32_t by, uint32_t n, uint32_t walkers) {
+        for (i += by; i >= n; i -= n) tile += walkers;
     }
 };
 // A place in a ring of `size` buffers and the parity of its turn
@@ -138,17 +195,17 @@ struct Ring {
     }
 };
 
-template <typename T, int P, bool TMA>
+template <typename T, int P, bool TMA, bool PAIR>
 __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1)
     int4_mma_kernel(const __grid_constant__ MmaArgs p) {
+    static_assert(TMA || !PAIR, "a pair copies its dense operand by TMA");
     extern __shared__ __align__(1024) uint8_t smem[];
-    constexpr uint32_t kSlotSteps = Shape<P>::kSlotSteps, kRawBytes = Shape<P>::kRawBytes;
+    constexpr uint32_t kSlotSteps = Shape<P>::kSlotSteps, kRawBytes = Shape<P>::kRawBytes, kWide = PAIR ? 256 : 128;
     const Int4Args &a = p.a;
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
     const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
     const uint32_t stage_bytes = kQuantBytes + p.dense_bytes;
-    const uint32_t raw0 = base + p.stages * stage_bytes, joint0 = raw0 + p.raws * kRawBytes;
-    const uint32_t bars = joint0 + Shape<P>::kJointBytes;
+    const uint32_t raw0 = base + p.stages * stage_bytes, bars = raw0 + p.raws * kRawBytes;
     auto quant_full = [&](uint32_t i) { return bars + 8 * i; };
     auto dense_full = [&](uint32_t i) { return bars + 64 + 8 * i; };
     auto stage_free = [&](uint32_t i) { return bars + 128 + 8 * i; };
@@ -157,17 +214,22 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
     auto acc_full = [&](uint32_t i) { return bars + 320 + 8 * i; };
     auto acc_free = [&](uint32_t i) { return bars + 336 + 8 * i; };
     const uint32_t tmem_slot = bars + 352;
-    // this CTA's share of the contraction (whole raw slots); the tile's first o (forward) or k, and its
-    // first token or (scale gradient) o
-    const uint32_t splits = gridDim.y, rank = blockIdx.y;
+    // the walkers over tiles are CTAs or pairs; `half` is this CTA's place in its pair
+    const uint32_t half = PAIR ? blockIdx.x & 1u : 0u, walker = PAIR ? blockIdx.x / 2 : blockIdx.x;
+    const uint32_t walkers = PAIR ? gridDim.x / 2 : gridDim.x;
+    // this CTA's share of the contraction (whole raw slots)
+    const uint32_t splits = PAIR ? 1 : gridDim.y, rank = PAIR ? 0 : blockIdx.y;
     const uint32_t slot_lo = uint32_t(uint64_t(rank) * p.slots / splits), slot_hi = uint32_t(uint64_t(rank + 1) * p.slots / splits);
     const uint32_t step_lo = slot_lo * kSlotSteps, steps = min(slot_hi * kSlotSteps, p.steps) - step_lo;
-    auto first_a = [&](uint32_t tile) { return 128 * (tile / p.tiles_b); };
-    auto first_b = [&](uint32_t tile) { return int64_t(tile % p.tiles_b) * p.bn; };
+    // a tile's first index of D's rows (this CTA's 128 of them) and of its columns
+    auto row0 = [&](uint32_t tile) { return kWide * (tile / p.tiles_b) + 128 * half; };
+    auto col0 = [&](uint32_t tile) { return int64_t(tile % p.tiles_b) * p.bn; };
+    // the first of the CTA's 128 features of the quantized operand: o (forward) or k
+    auto quant0 = [&](uint32_t tile) { return P == kScaleGrad ? uint32_t(col0(tile)) + 128 * half : row0(tile); };
 
     if (threadIdx.x == 0) {
         for (uint32_t i = 0; i < p.stages; ++i) {
-            mbar_init(quant_full(i), 4);
+            mbar_init(quant_full(i), PAIR ? 8 : 4);
             mbar_init(dense_full(i), TMA ? 1 : kLoadWarps);
             mbar_init(stage_free(i), 1);
         }
@@ -177,24 +239,30 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
         }
         for (uint32_t i = 0; i < 2; ++i) {
             mbar_init(acc_full(i), 1);
-            mbar_init(acc_free(i), kOutWarps);
+            mbar_init(acc_free(i), PAIR ? 2 * kOutWarps : kOutWarps);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async();
     }
     if (warp == kMmaWarp) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tmem_slot), "r"(p.tmem_cols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        if constexpr (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tmem_slot), "r"(p.tmem_cols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tmem_slot), "r"(p.tmem_cols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
+    if constexpr (PAIR) cluster_sync();  // the other CTA's barriers are ready
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = lds32(tmem_slot);
     uint32_t err = 0;
-    // sums for the cluster lie where the stages were (one tile a CTA then), the scale gradient's otherwise
-    // in their own place
-    float *joint = reinterpret_cast<float *>(smem + (P == kScaleGrad && splits == 1 ? joint0 - base : 0u));
+    // sums for the cluster lie where the stages were (one tile a CTA then)
+    float *joint = reinterpret_cast<float *>(smem);
 
     if (warp < kExpandWarps) {
         // ---- expand the quantized operand: group warp / 4 takes every kGroups-th step, a row of 64 elements
@@ -205,10 +273,10 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
         // the thread's scales in a step (0 where there is none), read one step ahead
         auto load_scales = [&](const Walk &w) {
             if (w.tile >= p.tiles) return;
-            const uint32_t a0 = first_a(w.tile), step = step_lo + w.i;
+            const uint32_t a0 = quant0(w.tile), step = step_lo + w.i;
             if constexpr (P == kScaleGrad) {
                 const uint32_t t = 64 * step + (r & 63u);
-                scale[0] = t < a.m ? __float_as_uint(__ldg(a.act_scales + int64_t(t) * a.act_groups + a0 / 128)) : 0u;
+                scale[0] = t < a.m && a0 < a.k ? __float_as_uint(__ldg(a.act_scales + int64_t(t) * a.act_groups + a0 / 128)) : 0u;
             } else {
                 const uint32_t o = P == kForward ? a0 + r : 64 * step + (r & 63u);
                 const uint32_t k = P == kForward ? 64 * step : a0 + 64 * cc;
@@ -217,14 +285,14 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
                 scale[1] = o < a.n && k + 32 < a.k ? __ldg(row + (k + 32) / a.group) : 0u;
             }
         };
-        Walk mine{blockIdx.x, 0};  // this group's next step
-        mine.advance(group, steps);
+        Walk mine{walker, 0};  // this group's next step
+        mine.advance(group, steps, walkers);
         Ring stage, raw;
         stage.advance(group, p.stages);
         load_scales(mine);
         // every group passes every slot, in order, and frees it, whether it has a step there or not: none is
         // ever further ahead of another than the ring is long, so no turn is taken for another
-        for (Walk at{blockIdx.x, 0}; at.tile < p.tiles; raw.advance(1, p.raws)) {
+        for (Walk at{walker, 0}; at.tile < p.tiles; raw.advance(1, p.raws)) {
             if (!mbar_wait(raw_full(raw.at), raw.phase)) {
                 err = EP_DEC_TIMEOUT;
                 break;
@@ -232,14 +300,14 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
             const uint32_t left = min(kSlotSteps, steps - at.i), js = mine.i - at.i;
             const bool has = mine.tile == at.tile && js < left;
             at.i += left;
-            if (at.i == steps) at.i = 0, at.tile += gridDim.x;
+            if (at.i == steps) at.i = 0, at.tile += walkers;
             if (!has) {
                 __syncwarp();
-                if (lane == 0) mbar_arrive(raw_free(raw.at), 1);
+                if (lane == 0) mbar_arrive(raw_free(raw.at));
                 continue;
             }
             const uint32_t now[2] = {scale[0], scale[1]};
-            mine.advance(kGroups, steps);
+            mine.advance(kGroups, steps, walkers);
             load_scales(mine);
             const uint32_t src = raw0 + raw.at * kRawBytes;
             uint32_t out[8][4];
@@ -279,7 +347,7 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(raw_free(raw.at), 1);
+            if (lane == 0) mbar_arrive(raw_free(raw.at));
             if (!mbar_wait(stage_free(stage.at), stage.phase ^ 1u)) {
                 err = EP_DEC_TIMEOUT;
                 break;
@@ -289,69 +357,53 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
             for (uint32_t i = 0; i < 8; ++i) sts128(dst + 16 * (i ^ (r & 7u)), out[i]);
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(quant_full(stage.at), 1);
+            if (lane == 0) arrive_issuer<PAIR>(quant_full(stage.at));
             stage.advance(kGroups, p.stages);
         }
     } else if (warp < kMmaWarp) {
         // ---- the output: warp q of the four reads lanes 32 q .. of the accumulator
         const uint32_t q = warp - kOutWarp0;
         Ring acc;
-        for (uint32_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x, acc.advance(1, 2)) {
-            const uint32_t a0 = first_a(tile);
-            const int64_t b0 = first_b(tile);
-            // after a lost wait the warps still meet at their barriers (and wait no more)
-            if (!err && !mbar_wait(acc_full(acc.at), acc.phase)) err = EP_DEC_TIMEOUT;
+        for (uint32_t tile = walker; tile < p.tiles; tile += walkers, acc.advance(1, 2)) {
+            const uint32_t a0 = row0(tile);
+            const int64_t b0 = col0(tile);
+            if (!mbar_wait(acc_full(acc.at), acc.phase)) {
+                err = EP_DEC_TIMEOUT;
+                break;
+            }
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t from = tmem + ((32u * q) << 16) + acc.at * p.bn;
             if constexpr (P == kScaleGrad) {
-                // lane: input k; a column (output feature) times the codes, summed over the warp's 32 inputs
-                // by exchanging halves (16 shuffles for 16 columns, after which lanes l and l + 16 have column
-                // l's sum); then the warps of a group and the cluster's CTAs, in order
-                const uint32_t k = a0 + 32 * q + lane, place = 4 * ((k & 7u) / 2) + 16 * (k & 1u), o0 = uint32_t(b0);
-                const uint32_t *codes = a.codes + k / 8;
-                uint32_t w[16];
-                auto load_codes = [&](uint32_t c) {
+                // lane: output feature o; its row of D times its codes, summed over 32 inputs, then over a group
+                const uint32_t o = a0 + 32 * q + lane;
+                const uint4 *codes = reinterpret_cast<const uint4 *>(a.codes + int64_t(min(o, a.n - 1)) * a.words + b0 / 8);
+                uint16_t *out = a.out + int64_t(o) * a.groups + b0 / a.group;
+                float sum = 0.0f;
+                for (uint32_t c = 0; c < kWide / 32; ++c) {  // 32 inputs: 16 bytes of codes
+                    const uint32_t k = uint32_t(b0) + 32 * c;
+                    const uint4 v = k < 8 * a.words ? __ldg(codes + c) : make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    float s = 0.0f;
 #pragma unroll
-                    for (uint32_t i = 0; i < 16; ++i)
-                        w[i] = o0 + c + i < a.n && k / 8 < a.words ? __ldg(codes + int64_t(o0 + c + i) * a.words) : 0x88888888u;
-                };
-                load_codes(0);
-                for (uint32_t c = 0; c < 256; c += 16) {
-                    uint32_t d[16];
-                    tmem_load16(d, from + c);
-                    float v[16];
+                    for (uint32_t h = 0; h < 2; ++h) {
+                        uint32_t d[16];
+                        tmem_load16(d, from + 32 * c + 16 * h);
 #pragma unroll
-                    for (uint32_t i = 0; i < 16; ++i) v[i] = __uint_as_float(d[i]) * float(int((w[i] >> place) & 15u) - 8);
-                    if (c + 16 < 256) load_codes(c + 16);
-#pragma unroll
-                    for (uint32_t s = 8; s > 0; s >>= 1) {
-                        const bool up = lane & s;
-#pragma unroll
-                        for (uint32_t i = 0; i < s; ++i) {
-                            const float got = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + s], s);
-                            v[i] = (up ? v[i + s] : v[i]) + got;
+                        for (uint32_t e = 0; e < 16; ++e) {
+                            const uint32_t in = e & 7u, code = (w[2 * h + e / 8] >> (4 * (in / 2) + 16 * (in & 1u))) & 15u;
+                            s = fmaf(__uint_as_float(d[e]), float(int(code) - 8), s);
                         }
                     }
-                    v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
                     if (splits > 1) {
-                        if (lane < 16) joint[256 * q + c + lane] = v[0];
+                        joint[4 * (32 * q + lane) + c] = s;
                         continue;
                     }
-                    if (lane < 16) joint[128 * q + (c & 127u) + lane] = v[0];
-                    if ((c & 127u) != 112) continue;
-                    named_sync(1, 32 * kOutWarps);
-                    const uint32_t per = 128 / a.group, span = 4 / per;
-                    for (uint32_t e = 32 * q + lane; e < 128 * per; e += 32 * kOutWarps) {
-                        const uint32_t row = o0 + c - 112 + e / per, i = e % per, g = a0 / a.group + i;
-                        float s = 0.0f;
-                        for (uint32_t h = i * span; h < (i + 1) * span; ++h) s += joint[128 * h + e / per];
-                        if (row < a.n && g < a.groups) a.out[int64_t(row) * a.groups + g] = Elem<T>::bits(s);
+                    sum += s;
+                    if ((32 * (c + 1)) % a.group == 0) {  // a group's end (groups do not cross tiles)
+                        if (o < a.n && b0 / a.group + c * 32 / a.group < a.groups) out[c * 32 / a.group] = Elem<T>::bits(sum);
+                        sum = 0.0f;
                     }
-                    named_sync(1, 32 * kOutWarps);  // the sums are read before the next ones
                 }
-                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(acc_free(acc.at), 1);
             } else {
                 const uint32_t J = P == kForward ? a.n : a.k, f = 32 * q + lane, j = a0 + f;
                 const float b = P == kForward && a.bias && j < J ? Elem<T>::f(__ldg(a.bias + j)) : 0.0f;
@@ -368,21 +420,21 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
                                 a.out[(b0 + c + i) * J + j] = Elem<T>::bits(__uint_as_float(d[i]) * Codes<T>::kUnit + b);
                     }
                 }
-                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(acc_free(acc.at), 1);
             }
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) arrive_issuer<PAIR>(acc_free(acc.at));
         }
     } else if (warp == kMmaWarp) {
         // ---- the matrix instructions, 16 of the contraction each
         Ring stage, acc;
-        for (uint32_t tile = blockIdx.x; tile < p.tiles && !err; tile += gridDim.x, acc.advance(1, 2)) {
-            if (!mbar_wait(acc_free(acc.at), acc.phase ^ 1u)) {
+        for (uint32_t tile = walker; half == 0 && tile < p.tiles && !err; tile += walkers, acc.advance(1, 2)) {
+            if (!wait_pair<PAIR>(acc_free(acc.at), acc.phase ^ 1u)) {
                 err = EP_DEC_TIMEOUT;
                 break;
             }
             for (uint32_t i = 0; i < steps; ++i) {
-                if (!mbar_wait(quant_full(stage.at), stage.phase) || !mbar_wait(dense_full(stage.at), stage.phase)) {
+                if (!wait_pair<PAIR>(quant_full(stage.at), stage.phase) || !wait_pair<PAIR>(dense_full(stage.at), stage.phase)) {
                     err = EP_DEC_TIMEOUT;
                     break;
                 }
@@ -392,16 +444,19 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
 #pragma unroll
                     for (uint32_t h = 0; h < 4; ++h) {
                         const uint32_t more = i > 0 || h > 0;
-                        const uint64_t da = P == kForward ? desc128(quant + 32 * h, 0) : desc128(quant + 2048 * h, 8192);
-                        const uint64_t db = P == kScaleGrad ? desc128(dense + 2048 * h, 8192) : desc128(dense + 32 * h, 0);
-                        mma_f16(d, da, db, p.idesc, more);
+                        if constexpr (P == kForward)
+                            mma_f16<PAIR>(d, desc128(quant + 32 * h, 0), desc128(dense + 32 * h, 0), p.idesc, more);
+                        else if constexpr (P == kInputGrad)
+                            mma_f16<PAIR>(d, desc128(quant + 2048 * h, 8192), desc128(dense + 32 * h, 0), p.idesc, more);
+                        else
+                            mma_f16<PAIR>(d, desc128(dense + 2048 * h, 8192), desc128(quant + 2048 * h, 8192), p.idesc, more);
                     }
-                    mma_commit(stage_free(stage.at));
+                    mma_commit<PAIR>(stage_free(stage.at));
                 }
                 __syncwarp();
                 stage.advance(1, p.stages);
             }
-            if (lane == 0) mma_commit(acc_full(acc.at));
+            if (lane == 0) mma_commit<PAIR>(acc_full(acc.at));
             __syncwarp();
         }
     } else if (warp == kRawWarp) {
@@ -409,8 +464,8 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
         if (lane == 0) {
             Ring raw;
             uint32_t copies = 0;
-            for (uint32_t tile = blockIdx.x; tile < p.tiles && !err; tile += gridDim.x) {
-                const uint32_t a0 = first_a(tile);
+            for (uint32_t tile = walker; tile < p.tiles && !err; tile += walkers) {
+                const uint32_t a0 = quant0(tile);
                 for (uint32_t slot = slot_lo; slot < slot_hi; ++slot, ++copies, raw.advance(1, p.raws)) {
                     if (!mbar_wait(raw_free(raw.at), raw.phase ^ 1u)) {
                         err = EP_DEC_TIMEOUT;
@@ -436,8 +491,8 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
         if (lane == 0) {
             Ring stage;
             uint32_t copies = 0;
-            for (uint32_t tile = blockIdx.x; tile < p.tiles && !err; tile += gridDim.x) {
-                const uint32_t b0 = uint32_t(first_b(tile));
+            for (uint32_t tile = walker; tile < p.tiles && !err; tile += walkers) {
+                const uint32_t b0 = P == kScaleGrad ? row0(tile) : uint32_t(col0(tile)) + (PAIR ? p.bn / 2 : 0u) * half;
                 for (uint32_t i = 0; i < steps; ++i, ++copies, stage.advance(1, p.stages)) {
                     if (!mbar_wait(stage_free(stage.at), stage.phase ^ 1u)) {
                         err = EP_DEC_TIMEOUT;
@@ -445,26 +500,35 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
                     }
                     const uint32_t dst = base + stage.at * stage_bytes + kQuantBytes, bar = dense_full(stage.at);
                     const uint32_t c = 64 * (step_lo + i);
-                    mbar_expect(bar, p.dense_bytes);
+                    const auto load = [&](uint32_t at, uint32_t col, uint32_t row) {
+                        if constexpr (PAIR)
+                            tma_load_pair(at, &p.dense, col, row, bar);
+                        else
+                            tma_load(at, &p.dense, col, row, bar);
+                    };
+                    if (half == 0) mbar_expect(bar, (PAIR ? 2 : 1) * p.dense_bytes);  // both halves
                     if constexpr (P == kScaleGrad) {
-#pragma unroll
-                        for (uint32_t h = 0; h < 4; ++h) tma_load(dst + 8192 * h, &p.dense, b0 + 64 * h, c, bar);
+                        load(dst, b0, c);
+                        load(dst + 8192, b0 + 64, c);
                     } else {
-                        tma_load(dst, &p.dense, c, b0, bar);
+                        load(dst, c, b0);
                     }
                 }
             }
+            // (a pair's barriers are the first CTA's; the second's copies are done when its last stages are free)
             for (uint32_t i = copies > p.stages ? copies - p.stages : 0; i < copies; ++i)
-                if (!mbar_wait(dense_full(i % p.stages), (i / p.stages) & 1u)) err = EP_DEC_TIMEOUT;
+                if (half == 0 ? !mbar_wait(dense_full(i % p.stages), (i / p.stages) & 1u)
+                              : !mbar_wait(stage_free(i % p.stages), (i / p.stages) & 1u))
+                    err = EP_DEC_TIMEOUT;
         }
         __syncwarp();
     } else {
         // ---- the dense operand through registers: 16-byte chunks of 8 elements, each checked
-        const uint32_t rows = P == kScaleGrad ? 64 : p.bn, boxes = P == kScaleGrad ? 4 : 1;
+        const uint32_t rows = P == kScaleGrad ? 64 : p.bn, boxes = P == kScaleGrad ? 2 : 1;
         const uint32_t cols_all = P == kForward ? a.k : a.n;
         Ring stage;
-        for (uint32_t tile = blockIdx.x; tile < p.tiles && !err; tile += gridDim.x) {
-            const int64_t b0 = first_b(tile);
+        for (uint32_t tile = walker; tile < p.tiles && !err; tile += walkers) {
+            const int64_t b0 = P == kScaleGrad ? int64_t(row0(tile)) : col0(tile);
             for (uint32_t i = 0; i < steps; ++i, stage.advance(1, p.stages)) {
                 const uint32_t step = step_lo + i;
                 if (!mbar_wait(stage_free(stage.at), stage.phase ^ 1u)) {
@@ -495,24 +559,24 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
                 }
                 fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(dense_full(stage.at), 1);
+                if (lane == 0) mbar_arrive(dense_full(stage.at));
             }
         }
     }
 
     // ---- a split contraction: each CTA adds its share of the tile over the cluster
     if (splits > 1) {
-        const uint32_t a0 = first_a(blockIdx.x);
-        const int64_t b0 = first_b(blockIdx.x);
+        const uint32_t a0 = row0(walker);
+        const int64_t b0 = col0(walker);
         cluster_sync();
         if constexpr (P == kScaleGrad) {
-            const uint32_t per = 128 / a.group, span = 4 / per, o0 = uint32_t(b0);
-            for (uint32_t e = rank * blockDim.x + threadIdx.x; e < 256 * per; e += splits * blockDim.x) {
-                const uint32_t row = o0 + e / per, i = e % per, g = a0 / a.group + i;
+            const uint32_t per = 128 / a.group, span = 4 / per;
+            for (uint32_t e = rank * blockDim.x + threadIdx.x; e < 128 * per; e += splits * blockDim.x) {
+                const uint32_t o = a0 + e / per, i = e % per, g = uint32_t(b0) / a.group + i;
                 float s = 0.0f;
                 for (uint32_t c = 0; c < splits; ++c)
-                    for (uint32_t h = i * span; h < (i + 1) * span; ++h) s += ld_cluster(&joint[256 * h + e / per], c);
-                if (row < a.n && g < a.groups) a.out[int64_t(row) * a.groups + g] = Elem<T>::bits(s);
+                    for (uint32_t h = i * span; h < (i + 1) * span; ++h) s += ld_cluster(&joint[4 * (e / per) + h], c);
+                if (o < a.n && g < a.groups) a.out[int64_t(o) * a.groups + g] = Elem<T>::bits(s);
             }
         } else {
             const uint32_t J = P == kForward ? a.n : a.k, f = threadIdx.x & 127u, j = a0 + f, rows = blockDim.x / 128;
@@ -530,9 +594,13 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
     if (err && a.status && lane == 0) atomicOr(a.status, err);
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
+    if constexpr (PAIR) cluster_sync();  // neither CTA leaves while the other still reads or signals it
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(p.tmem_cols) : "memory");
+        if constexpr (PAIR)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(p.tmem_cols) : "memory");
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(p.tmem_cols) : "memory");
     }
 }
 
@@ -566,7 +634,7 @@ int device_sms() {
 }
 constexpr size_t kSmemMost = 232448;
 
-// the launch: tiles, the contraction's split, rings as deep as fit
+// the launch: single or paired CTAs, tiles, the contraction's split, rings as deep as fit
 template <typename T, int P>
 int launch_mma(const Int4Args &a, int sms, cudaStream_t s) {
     MmaArgs p{};
@@ -574,68 +642,79 @@ int launch_mma(const Int4Args &a, int sms, cudaStream_t s) {
     const int64_t contraction = P == kForward ? a.k : P == kInputGrad ? int64_t(a.n) : a.m;
     p.steps = uint32_t((contraction + 63) / 64);
     p.slots = (p.steps + Shape<P>::kSlotSteps - 1) / Shape<P>::kSlotSteps;
-    uint64_t tiles_a, tiles_b;
-    tiles_a = ((P == kForward ? a.n : a.k) + 127) / 128;
-    if (P == kScaleGrad) {
-        p.bn = 256;
-        tiles_b = (a.n + 255) / 256;
-    } else {
-        tiles_b = uint64_t(a.m + 255) / 256;
-        p.bn = uint32_t(((a.m + int64_t(tiles_b) - 1) / int64_t(tiles_b) + 15) / 16 * 16);
-    }
-    p.dense_bytes = p.bn * 128;
-    if (tiles_a * tiles_b > 0x7fffffff) return EP_ERR_UNSUPPORTED;
-    p.tiles = uint32_t(tiles_a * tiles_b);
-    p.tiles_b = uint32_t(tiles_b);
-    uint32_t splits = 1;
-    if (p.tiles < uint32_t(sms)) splits = std::max(1u, std::min({8u, sms / p.tiles, p.slots / (P == kScaleGrad ? 4u : 1u)}));
-    const uint32_t stage = kQuantBytes + p.dense_bytes, raw = Shape<P>::kRawBytes, fixed = kBarBytes + Shape<P>::kJointBytes;
-    p.raws = P == kScaleGrad ? 4 : 2;
-    p.stages = std::min<uint32_t>(kMaxStages, uint32_t((kSmemMost - fixed - p.raws * raw) / stage));
-    p.raws = std::min<uint32_t>(kMaxRaws, uint32_t((kSmemMost - fixed - p.stages * stage) / raw));
-    // a group waits for the matrix instructions that read its stage last; it has seen those of the turn
-    // before done only if the ring holds a step of every group
-    if (p.stages < kGroups) return EP_ERR_UNSUPPORTED;
-    const size_t bytes = size_t(p.stages) * stage + size_t(p.raws) * raw + fixed;
-    // accumulator fp32, A and B of T; the scale gradient's operands and the input gradient's weight MN-major
-    const uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-    p.idesc = (1u << 4) | (type << 7) | (type << 10) | (P != kForward ? 1u << 15 : 0u) | (P == kScaleGrad ? 1u << 16 : 0u) |
-              ((p.bn >> 3) << 17) | ((128u >> 4) << 24);
-    p.tmem_cols = 32;
-    while (p.tmem_cols < 2 * p.bn) p.tmem_cols *= 2;
     const uint64_t dense_cols = P == kForward ? a.k : a.n;
     const int64_t ld = a.m > 1 ? a.ldx : int64_t((dense_cols + 7) / 8 * 8);
     const bool tma = !misaligned(a.x, 16) && ld % 8 == 0 && ld < (int64_t(1) << 38) && a.m <= 0x7fffffff;
     p.dense_align = !misaligned(a.x, 4) && ld % 2 == 0 ? 4 : 2;
+    const uint64_t rows = P == kInputGrad ? a.k : a.n, cols = P == kScaleGrad ? a.k : uint64_t(a.m);
+    // pairs where their tiles (256 x 256) keep most SMs busy
+    const bool pair = tma && cols > 128 && ((rows + 255) / 256) * ((cols + 255) / 256) * 8 >= uint64_t(sms) * 3;
+    const uint64_t tiles_a = pair ? (rows + 255) / 256 : (rows + 127) / 128;
+    uint64_t tiles_b;
+    if (P == kScaleGrad) {
+        p.bn = pair ? 256 : 128;
+        tiles_b = (cols + p.bn - 1) / p.bn;
+        p.dense_bytes = 16384;
+    } else {
+        const uint32_t unit = pair ? 32 : 16;
+        tiles_b = (cols + 255) / 256;
+        p.bn = uint32_t(((cols + tiles_b - 1) / tiles_b + unit - 1) / unit * unit);
+        p.dense_bytes = (pair ? p.bn / 2 : p.bn) * 128;
+    }
+    if (tiles_a * tiles_b > 0x3fffffff) return EP_ERR_UNSUPPORTED;
+    p.tiles = uint32_t(tiles_a * tiles_b);
+    p.tiles_b = uint32_t(tiles_b);
+    uint32_t splits = 1;
+    if (!pair && p.tiles < uint32_t(sms))
+        splits = std::max(1u, std::min({8u, sms / p.tiles, p.slots / (P == kScaleGrad ? 4u : 1u)}));
+    const uint32_t stage = kQuantBytes + p.dense_bytes, raw = Shape<P>::kRawBytes;
+    p.raws = P == kScaleGrad ? 4 : 2;
+    p.stages = std::min<uint32_t>(kMaxStages, uint32_t((kSmemMost - kBarBytes - p.raws * raw) / stage));
+    p.raws = std::min<uint32_t>(kMaxRaws, uint32_t((kSmemMost - kBarBytes - p.stages * stage) / raw));
+    // a group waits for the matrix instructions that read its stage last; it has seen those of the turn
+    // before done only if the ring holds a step of every group
+    if (p.stages < kGroups) return EP_ERR_UNSUPPORTED;
+    const size_t bytes = size_t(p.stages) * stage + size_t(p.raws) * raw + kBarBytes;
+    // accumulator fp32, A and B of T; the scale gradient's operands and the input gradient's weight MN-major
+    const uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+    p.idesc = (1u << 4) | (type << 7) | (type << 10) | (P != kForward ? 1u << 15 : 0u) | (P == kScaleGrad ? 1u << 16 : 0u) |
+              ((p.bn >> 3) << 17) | (((pair ? 256u : 128u) >> 4) << 24);
+    p.tmem_cols = 32;
+    while (p.tmem_cols < 2 * p.bn) p.tmem_cols *= 2;
     const CUtensorMapDataType dt = type ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     const uint64_t pitch = P == kScaleGrad ? uint64_t(act8_row_bytes(a.k)) : uint64_t(a.words) * 4;
     const void *quant = P == kScaleGrad ? static_cast<const void *>(a.act) : static_cast<const void *>(a.codes);
     if (!tensor_map(&p.raw, quant, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, pitch, P == kScaleGrad ? uint64_t(a.m) : a.n, pitch,
                     P == kInputGrad ? 64 : 128, P == kForward ? 128 : P == kInputGrad ? 256 : 64))
         return EP_ERR_CUDA;
-    if (tma && !tensor_map(&p.dense, a.x, dt, 2, dense_cols, uint64_t(a.m), uint64_t(ld) * 2, 64, P == kScaleGrad ? 64 : p.bn))
+    if (tma && !tensor_map(&p.dense, a.x, dt, 2, dense_cols, uint64_t(a.m), uint64_t(ld) * 2, 64,
+                           P == kScaleGrad ? 64 : p.dense_bytes / 128))
         return EP_ERR_CUDA;
-    const auto kern = tma ? int4_mma_kernel<T, P, true> : int4_mma_kernel<T, P, false>;
-    static std::atomic<uint64_t> allowed[2];  // devices on which the kernel may use kSmemMost
+    const uint32_t form = pair ? 2 : tma ? 1 : 0;
+    const auto kern = pair  ? int4_mma_kernel<T, P, true, true>
+                      : tma ? int4_mma_kernel<T, P, true, false>
+                            : int4_mma_kernel<T, P, false, false>;
+    static std::atomic<uint64_t> allowed[3];  // devices on which the kernel may use kSmemMost
     int device = 0;
     if (cudaGetDevice(&device) != cudaSuccess || device < 0 || device >= 64) return EP_ERR_CUDA;
-    if (!(allowed[tma].load() >> device & 1u)) {
+    if (!(allowed[form].load() >> device & 1u)) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemMost)) != cudaSuccess)
             return EP_ERR_CUDA;
-        allowed[tma].fetch_or(uint64_t(1) << device);
+        allowed[form].fetch_or(uint64_t(1) << device);
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(splits > 1 ? p.tiles : std::min(p.tiles, uint32_t(sms)), splits);
+    cfg.gridDim = pair ? dim3(2 * std::min(p.tiles, uint32_t(sms) / 2))
+                       : dim3(splits > 1 ? p.tiles : std::min(p.tiles, uint32_t(sms)), splits);
     cfg.blockDim = dim3((kDenseWarp0 + (tma ? 1 : kLoadWarps)) * 32);
     cfg.dynamicSmemBytes = bytes;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.x = pair ? 2 : 1;
     attr[0].val.clusterDim.y = splits;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = splits > 1 ? 1 : 0;
+    cfg.numAttrs = pair || splits > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
 }
 template <int P>

@@ -267,7 +267,9 @@ SHAPES = [(1, 1, 1, 32), (1, 64, 64, 32), (1, 1024, 1024, 128), (1, 130, 257, 64
           (5, 2050, 640, 64), (7, 129, 1000, 64), (8, 256, 2048, 128), (9, 96, 320, 32), (16, 128, 128, 128), (17, 300, 72, 32),
           (33, 200, 1027, 32), (48, 512, 1024, 128), (64, 1024, 96, 64), (100, 65, 130, 128), (128, 256, 512, 64),
           (129, 128, 256, 32), (200, 300, 400, 128), (256, 640, 64, 32), (257, 130, 70, 32), (512, 256, 1088, 64),
-          (1000, 515, 130, 128)]
+          (1000, 515, 130, 128),
+          # many tiles, ragged in every direction: two CTAs to a tile, several tiles each
+          (2040, 2104, 72, 32), (2040, 72, 2100, 64), (70, 2104, 1990, 32), (2300, 2048, 2304, 128), (700, 5000, 5100, 64)]
 
 
 @pytest.mark.gpu
