@@ -106,33 +106,9 @@ __device__ __forceinline__ uint32_t in_first(uint32_t addr) {
 template <bool PAIR>
 __device__ __forceinline__ void arrive_issuer(uint32_t bar) {
     if constexpr (PAIR)
-        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_first(bar)) : "memory");
+        asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(in_first(bar)) : "memory");
     else
         mbar_arrive(bar);
-}
-// mbar_wait for a barrier that the other CTA arrives on
-template <bool PAIR>
-__device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity) {
-    if constexpr (!PAIR) return mbar_wait(bar, parity);
-    for (uint32_t i = 0; i < kWaitLimit; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, "
-            "p;\n}\n"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
-        if (ok) return true;
-    }
-    return false;
-}
-// a box into this CTA's shared memory that completes on a barrier of the pair's first CTA
-__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap *map, uint32_t col, uint32_t row, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-        "[%4];" ::"r"(dst),
-        "l"(map), "r"(col), "r"(row), "r"(in_first(bar))
-        : "memory");
 }
 __device__ __forceinline__ void sts128(uint32_t a, const uint32_t (&v)[4]) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
@@ -206,8 +182,7 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
     const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
     const uint32_t stage_bytes = kQuantBytes + p.dense_bytes;
     const uint32_t raw0 = base + p.stages * stage_bytes, bars = raw0 + p.raws * kRawBytes;
-    auto quant_full = [&](uint32_t i) { return bars + 8 * i; };
-    auto dense_full = [&](uint32_t i) { return bars + 64 + 8 * i; };
+    auto full = [&](uint32_t i) { return bars + 8 * i; };  // both operands of a stage
     auto stage_free = [&](uint32_t i) { return bars + 128 + 8 * i; };
     auto raw_full = [&](uint32_t i) { return bars + 192 + 8 * i; };
     auto raw_free = [&](uint32_t i) { return bars + 256 + 8 * i; };
@@ -229,8 +204,8 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
 
     if (threadIdx.x == 0) {
         for (uint32_t i = 0; i < p.stages; ++i) {
-            mbar_init(quant_full(i), PAIR ? 8 : 4);
-            mbar_init(dense_full(i), TMA ? 1 : kLoadWarps);
+            // four expansion warps, the dense operand's copy (or its warps), the other CTA's stage
+            mbar_init(full(i), 4 + (TMA ? 1 : kLoadWarps) + (PAIR && half == 0 ? 1 : 0));
             mbar_init(stage_free(i), 1);
         }
         for (uint32_t i = 0; i < p.raws; ++i) {
@@ -357,7 +332,7 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
             for (uint32_t i = 0; i < 8; ++i) sts128(dst + 16 * (i ^ (r & 7u)), out[i]);
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) arrive_issuer<PAIR>(quant_full(stage.at));
+            if (lane == 0) mbar_arrive(full(stage.at));
             stage.advance(kGroups, p.stages);
         }
     } else if (warp < kMmaWarp) {
@@ -426,39 +401,44 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
             if (lane == 0) arrive_issuer<PAIR>(acc_free(acc.at));
         }
     } else if (warp == kMmaWarp) {
-        // ---- the matrix instructions, 16 of the contraction each
-        Ring stage, acc;
-        for (uint32_t tile = walker; half == 0 && tile < p.tiles && !err; tile += walkers, acc.advance(1, 2)) {
-            if (!wait_pair<PAIR>(acc_free(acc.at), acc.phase ^ 1u)) {
-                err = EP_DEC_TIMEOUT;
-                break;
-            }
-            for (uint32_t i = 0; i < steps; ++i) {
-                if (!wait_pair<PAIR>(quant_full(stage.at), stage.phase) || !wait_pair<PAIR>(dense_full(stage.at), stage.phase)) {
+        // ---- the matrix instructions, 16 of the contraction each, by one thread: little may lie between two
+        // steps' instructions, which take 512 cycles a step back to back (of 256 columns), 636 with two barriers
+        // and a warp's convergence between them.  A pair's second CTA passes on to the first that its stages
+        // are full
+        if (lane == 0) {
+            Ring stage, acc;
+            for (uint32_t tile = walker; tile < p.tiles && !err; tile += walkers, acc.advance(1, 2)) {
+                if (half == 0 && !mbar_wait(acc_free(acc.at), acc.phase ^ 1u)) {
                     err = EP_DEC_TIMEOUT;
                     break;
                 }
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                if (lane == 0) {
-                    const uint32_t quant = base + stage.at * stage_bytes, dense = quant + kQuantBytes, d = tmem + acc.at * p.bn;
-#pragma unroll
-                    for (uint32_t h = 0; h < 4; ++h) {
-                        const uint32_t more = i > 0 || h > 0;
-                        if constexpr (P == kForward)
-                            mma_f16<PAIR>(d, desc128(quant + 32 * h, 0), desc128(dense + 32 * h, 0), p.idesc, more);
-                        else if constexpr (P == kInputGrad)
-                            mma_f16<PAIR>(d, desc128(quant + 2048 * h, 8192), desc128(dense + 32 * h, 0), p.idesc, more);
-                        else
-                            mma_f16<PAIR>(d, desc128(dense + 2048 * h, 8192), desc128(quant + 2048 * h, 8192), p.idesc, more);
+                const uint32_t d = tmem + acc.at * p.bn;
+                for (uint32_t i = 0; i < steps; ++i) {
+                    if (!mbar_wait(full(stage.at), stage.phase)) {
+                        err = EP_DEC_TIMEOUT;
+                        break;
                     }
-                    mma_commit<PAIR>(stage_free(stage.at));
+                    if (half == 0) {
+                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                        const uint32_t quant = base + stage.at * stage_bytes, dense = quant + kQuantBytes;
+                        const uint64_t dq = desc128(quant, P == kForward ? 0 : 8192), dd = desc128(dense, P == kScaleGrad ? 8192 : 0);
+                        // a step of 16: 32 bytes along K-major rows, 16 rows of 128 bytes of the others
+                        constexpr uint64_t kQ = P == kForward ? 2 : 128, kD = P == kScaleGrad ? 128 : 2;
+#pragma unroll
+                        for (uint32_t h = 0; h < 4; ++h)
+                            mma_f16<PAIR>(d, P == kScaleGrad ? dd + h * kD : dq + h * kQ, P == kScaleGrad ? dq + h * kQ : dd + h * kD,
+                                          p.idesc, i > 0 || h > 0);
+                        mma_commit<PAIR>(stage_free(stage.at));
+                    } else {
+                        arrive_issuer<PAIR>(full(stage.at));
+                    }
+                    stage.advance(1, p.stages);
                 }
-                __syncwarp();
-                stage.advance(1, p.stages);
+                if (half == 0) mma_commit<PAIR>(acc_full(acc.at));
             }
-            if (lane == 0) mma_commit<PAIR>(acc_full(acc.at));
-            __syncwarp();
         }
+        __syncwarp();
     } else if (warp == kRawWarp) {
         // ---- the quantized operand's bytes, as buffers come free
         if (lane == 0) {
@@ -498,28 +478,19 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
                         err = EP_DEC_TIMEOUT;
                         break;
                     }
-                    const uint32_t dst = base + stage.at * stage_bytes + kQuantBytes, bar = dense_full(stage.at);
+                    const uint32_t dst = base + stage.at * stage_bytes + kQuantBytes, bar = full(stage.at);
                     const uint32_t c = 64 * (step_lo + i);
-                    const auto load = [&](uint32_t at, uint32_t col, uint32_t row) {
-                        if constexpr (PAIR)
-                            tma_load_pair(at, &p.dense, col, row, bar);
-                        else
-                            tma_load(at, &p.dense, col, row, bar);
-                    };
-                    if (half == 0) mbar_expect(bar, (PAIR ? 2 : 1) * p.dense_bytes);  // both halves
+                    mbar_expect(bar, p.dense_bytes);
                     if constexpr (P == kScaleGrad) {
-                        load(dst, b0, c);
-                        load(dst + 8192, b0 + 64, c);
+                        tma_load(dst, &p.dense, b0, c, bar);
+                        tma_load(dst + 8192, &p.dense, b0 + 64, c, bar);
                     } else {
-                        load(dst, c, b0);
+                        tma_load(dst, &p.dense, c, b0, bar);
                     }
                 }
             }
-            // (a pair's barriers are the first CTA's; the second's copies are done when its last stages are free)
             for (uint32_t i = copies > p.stages ? copies - p.stages : 0; i < copies; ++i)
-                if (half == 0 ? !mbar_wait(dense_full(i % p.stages), (i / p.stages) & 1u)
-                              : !mbar_wait(stage_free(i % p.stages), (i / p.stages) & 1u))
-                    err = EP_DEC_TIMEOUT;
+                if (!mbar_wait(full(i % p.stages), (i / p.stages) & 1u)) err = EP_DEC_TIMEOUT;
         }
         __syncwarp();
     } else {
@@ -559,7 +530,7 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
                 }
                 fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(dense_full(stage.at));
+                if (lane == 0) mbar_arrive(full(stage.at));
             }
         }
     }
