@@ -96,6 +96,11 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+    return one != 0;
+}
 // the address of a place of this CTA's shared memory in the pair's first CTA
 __device__ __forceinline__ uint32_t in_first(uint32_t addr) {
     uint32_t there;
@@ -109,6 +114,17 @@ __device__ __forceinline__ void arrive_issuer(uint32_t bar) {
         asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(in_first(bar)) : "memory");
     else
         mbar_arrive(bar);
+}
+// loads that stay where they are written (the compiler moves others down to their use, a whole step later)
+__device__ __forceinline__ uint32_t ldg_now32(const void *p) {
+    uint32_t v;
+    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint32_t ldg_now16(const void *p) {
+    uint16_t v;
+    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    return v;
 }
 __device__ __forceinline__ void sts128(uint32_t a, const uint32_t (&v)[4]) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
@@ -178,7 +194,9 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr uint32_t kSlotSteps = Shape<P>::kSlotSteps, kRawBytes = Shape<P>::kRawBytes, kWide = PAIR ? 256 : 128;
     const Int4Args &a = p.a;
-    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+    // (the shuffle tells the compiler that the role is the warp's: its loops' values then stay in uniform
+    // registers, which the matrix instructions take their operands from)
+    const uint32_t lane = threadIdx.x & 31u, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
     const uint32_t stage_bytes = kQuantBytes + p.dense_bytes;
     const uint32_t raw0 = base + p.stages * stage_bytes, bars = raw0 + p.raws * kRawBytes;
@@ -234,7 +252,7 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
     __syncthreads();
     if constexpr (PAIR) cluster_sync();  // the other CTA's barriers are ready
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    const uint32_t tmem = lds32(tmem_slot);
+    const uint32_t tmem = __shfl_sync(0xffffffffu, lds32(tmem_slot), 0);
     uint32_t err = 0;
     // sums for the cluster lie where the stages were (one tile a CTA then)
     float *joint = reinterpret_cast<float *>(smem);
@@ -244,6 +262,7 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
         // (128 bytes) a thread: row r of the 128, that is (forward) output feature r, or (input gradient, scale
         // gradient) output feature or token r % 64, inputs 64 (r / 64) .. of the tile's 128
         const uint32_t group = warp >> 2, r = 32 * (warp & 3u) + lane, cc = r >> 6;
+        const uint32_t group_bits = 31 - __clz(a.group);
         uint32_t scale[2];
         // the thread's scales in a step (0 where there is none), read one step ahead
         auto load_scales = [&](const Walk &w) {
@@ -251,13 +270,15 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
             const uint32_t a0 = quant0(w.tile), step = step_lo + w.i;
             if constexpr (P == kScaleGrad) {
                 const uint32_t t = 64 * step + (r & 63u);
-                scale[0] = t < a.m && a0 < a.k ? __float_as_uint(__ldg(a.act_scales + int64_t(t) * a.act_groups + a0 / 128)) : 0u;
+                scale[0] = 0u;
+                if (t < a.m && a0 < a.k) scale[0] = ldg_now32(a.act_scales + int64_t(t) * a.act_groups + a0 / 128);
             } else {
                 const uint32_t o = P == kForward ? a0 + r : 64 * step + (r & 63u);
                 const uint32_t k = P == kForward ? 64 * step : a0 + 64 * cc;
                 const uint16_t *row = a.scales + int64_t(o) * a.groups;
-                scale[0] = o < a.n && k < a.k ? __ldg(row + k / a.group) : 0u;
-                scale[1] = o < a.n && k + 32 < a.k ? __ldg(row + (k + 32) / a.group) : 0u;
+                scale[0] = scale[1] = 0u;
+                if (o < a.n && k < a.k) scale[0] = ldg_now16(row + (k >> group_bits));
+                if (o < a.n && k + 32 < a.k) scale[1] = ldg_now16(row + ((k + 32) >> group_bits));
             }
         };
         Walk mine{walker, 0};  // this group's next step
@@ -321,8 +342,6 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
                     }
                 }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(raw_free(raw.at));
             if (!mbar_wait(stage_free(stage.at), stage.phase ^ 1u)) {
                 err = EP_DEC_TIMEOUT;
                 break;
@@ -330,9 +349,14 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
             const uint32_t dst = base + stage.at * stage_bytes + 128 * r;
 #pragma unroll
             for (uint32_t i = 0; i < 8; ++i) sts128(dst + 16 * (i ^ (r & 7u)), out[i]);
+            // the stores are visible to the matrix unit, and the loads that fed them are done, so that the slot can
+            // be written again (freed before the stores, loads still under way returned the next slot's bytes)
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(full(stage.at));
+            if (lane == 0) {
+                mbar_arrive(full(stage.at));
+                mbar_arrive(raw_free(raw.at));
+            }
             stage.advance(kGroups, p.stages);
         }
     } else if (warp < kMmaWarp) {
@@ -401,44 +425,45 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
             if (lane == 0) arrive_issuer<PAIR>(acc_free(acc.at));
         }
     } else if (warp == kMmaWarp) {
-        // ---- the matrix instructions, 16 of the contraction each, by one thread: little may lie between two
-        // steps' instructions, which take 512 cycles a step back to back (of 256 columns), 636 with two barriers
-        // and a warp's convergence between them.  A pair's second CTA passes on to the first that its stages
-        // are full
-        if (lane == 0) {
-            Ring stage, acc;
-            for (uint32_t tile = walker; tile < p.tiles && !err; tile += walkers, acc.advance(1, 2)) {
-                if (half == 0 && !mbar_wait(acc_free(acc.at), acc.phase ^ 1u)) {
+        // ---- the matrix instructions, 16 of the contraction each, issued by one elected lane of a converged
+        // warp: little may lie between two steps' instructions, which take 512 cycles a step back to back (of
+        // 256 columns).  A pair's second CTA passes on to the first that its stages are full
+        const bool elected = elect_one();
+        Ring stage, acc;
+        for (uint32_t tile = walker; tile < p.tiles && !err; tile += walkers, acc.advance(1, 2)) {
+            if (half == 0 && !mbar_wait(acc_free(acc.at), acc.phase ^ 1u)) {
+                err = EP_DEC_TIMEOUT;
+                break;
+            }
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t d = tmem + acc.at * p.bn;
+            for (uint32_t i = 0; i < steps; ++i) {
+                const uint32_t quant = base + stage.at * stage_bytes, dense = quant + kQuantBytes;
+                const uint64_t dq = desc128(quant, P == kForward ? 0 : 8192), dd = desc128(dense, P == kScaleGrad ? 8192 : 0);
+                // a step of 16: 32 bytes along K-major rows, 16 rows of 128 bytes of the others
+                constexpr uint64_t kQ = P == kForward ? 2 : 128, kD = P == kScaleGrad ? 128 : 2;
+                if (!mbar_wait(full(stage.at), stage.phase)) {
                     err = EP_DEC_TIMEOUT;
                     break;
                 }
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const uint32_t d = tmem + acc.at * p.bn;
-                for (uint32_t i = 0; i < steps; ++i) {
-                    if (!mbar_wait(full(stage.at), stage.phase)) {
-                        err = EP_DEC_TIMEOUT;
-                        break;
-                    }
-                    if (half == 0) {
-                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                        const uint32_t quant = base + stage.at * stage_bytes, dense = quant + kQuantBytes;
-                        const uint64_t dq = desc128(quant, P == kForward ? 0 : 8192), dd = desc128(dense, P == kScaleGrad ? 8192 : 0);
-                        // a step of 16: 32 bytes along K-major rows, 16 rows of 128 bytes of the others
-                        constexpr uint64_t kQ = P == kForward ? 2 : 128, kD = P == kScaleGrad ? 128 : 2;
+                if (half == 0) {
+                    if (elected) {
 #pragma unroll
                         for (uint32_t h = 0; h < 4; ++h)
                             mma_f16<PAIR>(d, P == kScaleGrad ? dd + h * kD : dq + h * kQ, P == kScaleGrad ? dq + h * kQ : dd + h * kD,
                                           p.idesc, i > 0 || h > 0);
                         mma_commit<PAIR>(stage_free(stage.at));
-                    } else {
-                        arrive_issuer<PAIR>(full(stage.at));
                     }
-                    stage.advance(1, p.stages);
+                } else if (elected) {
+                    arrive_issuer<PAIR>(full(stage.at));
                 }
-                if (half == 0) mma_commit<PAIR>(acc_full(acc.at));
+                __syncwarp();
+                stage.advance(1, p.stages);
             }
+            if (half == 0 && elected) mma_commit<PAIR>(acc_full(acc.at));
+            __syncwarp();
         }
-        __syncwarp();
     } else if (warp == kRawWarp) {
         // ---- the quantized operand's bytes, as buffers come free
         if (lane == 0) {
