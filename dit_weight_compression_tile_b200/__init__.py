@@ -17,12 +17,12 @@ _LINEAR_NAMES = ("CompressedLinear", "CompressedFP8Linear", "CompressedINT8Linea
 
 def __getattr__(name):
     if name in _BINDING_NAMES:
-        from . import binding
-        return getattr(binding, name)
-    if name in _COMPRESSED_NAMES:
-        from . import compressed
-        return getattr(compressed, name)
-    if name in _LINEAR_NAMES:
-        from . import linear
-        return getattr(linear, name)
-    raise AttributeError(name)
+        from . import binding as module
+    elif name in _COMPRESSED_NAMES:
+        from . import compressed as module
+    elif name in _LINEAR_NAMES:
+        from . import linear as module
+    else:
+        raise AttributeError(name)
+    value = globals()[name] = getattr(module, name)  # looked up here once
+    return value

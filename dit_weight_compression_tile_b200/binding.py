@@ -4,6 +4,7 @@ Every step of compression runs in the library's C++ and every step of decompress
 its sm_100a kernel; this module passes torch tensors' pointers, sizes and streams.
 There is no fallback: a missing library or a missing GPU raises ``EpError``.
 """
+import contextlib
 import ctypes as C
 import os
 import re
@@ -488,44 +489,35 @@ def linear_fused(x, d_blob, info, tables, bias=None, out=None, work=None, status
 # ---------------------------------------------------------------- 4-bit weights with group scales
 INT4_GROUPS = (32, 64, 128)
 ACT8_GROUP = 128  # features per scale of an activation checkpoint
+_INT4_DTYPES = (torch.bfloat16, torch.float16)
 
 
-class _Launch:
-    """the device and stream of one call on CUDA tensors: entering makes the device and, where the
-    caller names a stream other than the current one, that stream current (outputs made inside
-    belong to it)"""
-    __slots__ = ("index", "stream", "back", "guard")
-
-    def __init__(self, t, stream):
-        self.index = t.device.index
-        self.stream, self.back, self.guard = stream, None, None
-
-    def __enter__(self):
-        if torch.cuda.current_device() != self.index:
-            self.back = torch.cuda.current_device()
-            torch.cuda.set_device(self.index)
-        if self.stream is None:
-            return torch.cuda.current_stream(self.index).cuda_stream
-        self.guard = torch.cuda.stream(self.stream)
-        self.guard.__enter__()
-        return self.stream.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
+# the current stream's handle without building a Stream object around it (1 us of a call of 10)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _rows(t, name, cols=None):
-    """a 2-D CUDA tensor whose rows are contiguous, with the distance between them"""
-    if t.dim() != 2 or not t.is_cuda:
-        raise EpError(-1, f"{name} must be a 2-D CUDA tensor")
-    if cols is not None and t.shape[1] != cols:
-        raise EpError(-1, f"{name} has {t.shape[1]} columns, not {cols}")
-    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        t = t.contiguous()
-    return t, (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+def _elsewhere(t, stream):
+    """whether a call on ``t`` must first make a device or a stream current"""
+    return stream is not None or torch.cuda.current_device() != t.device.index
+
+
+@contextlib.contextmanager
+def _made_current(t, stream):
+    """``t``'s device and ``stream`` (if given) as the current ones: what a call allocates belongs to the
+    stream that it launches on"""
+    with torch.cuda.device(t.device), torch.cuda.stream(stream):
+        yield
+
+
+def _rows(t):
+    """``t`` (2-D) with contiguous rows, and the distance between them"""
+    m, k = t.shape
+    ld, one = t.stride()
+    if (k > 1 and one != 1) or (m > 1 and ld < k):
+        t = t.detach().contiguous()
+        ld = k
+    return t, (ld if m > 1 else k)
 
 
 def _int4_weight(codes, scales, in_features, group):
@@ -534,22 +526,23 @@ def _int4_weight(codes, scales, in_features, group):
         raise EpError(-1, f"group must be one of {INT4_GROUPS}, not {group}")
     if in_features < 1:
         raise EpError(-1, "in_features must be at least 1")
-    if codes.dtype != torch.uint8 or codes.dim() != 2 or codes.shape[1] != (in_features + 31) // 32 * 16 \
-            or codes.shape[0] < 1 or not codes.is_contiguous() or not codes.is_cuda:
-        raise EpError(-1, f"codes must be a contiguous CUDA uint8 tensor of {(in_features + 31) // 32 * 16} bytes per row")
-    if scales is not None and (scales.dtype not in (torch.bfloat16, torch.float16) or not scales.is_contiguous()
-                               or tuple(scales.shape) != (codes.shape[0], -(-in_features // group))
-                               or scales.device != codes.device):
-        raise EpError(-1, f"scales must be contiguous BF16 or FP16 of shape {(codes.shape[0], -(-in_features // group))} "
-                          "on the codes' device")
-    return codes.shape[0]
+    row = (in_features + 31) // 32 * 16
+    if not codes.is_cuda or codes.dtype != torch.uint8 or codes.dim() != 2 or codes.shape[1] != row or codes.shape[0] < 1 \
+            or not codes.is_contiguous():
+        raise EpError(-1, f"codes must be a contiguous CUDA uint8 tensor of {row} bytes per row")
+    n = codes.shape[0]
+    if scales is not None and (scales.dtype not in _INT4_DTYPES or scales.shape != (n, -(-in_features // group))
+                               or not scales.is_contiguous() or scales.device != codes.device):
+        raise EpError(-1, f"scales must be contiguous BF16 or FP16 of shape {(n, -(-in_features // group))} on the codes' "
+                          "device")
+    return n
 
 
-def _output(out, shape, dtype, like, name="out"):
+def _output(out, like, shape, dtype):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    if out.device != like.device or out.dtype != dtype or tuple(out.shape) != tuple(shape) or not out.is_contiguous():
-        raise EpError(-1, f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {like.device}")
+        return like.new_empty(shape, dtype=dtype)
+    if out.device != like.device or out.dtype != dtype or out.shape != shape or not out.is_contiguous():
+        raise EpError(-1, f"out must be a contiguous {dtype} tensor of shape {tuple(shape)} on {like.device}")
     return out
 
 
@@ -567,23 +560,23 @@ def int4_quantize(weight, group=128, dtype=None, stream=None):
     group)) of ``dtype`` (torch.bfloat16 or torch.float16; default the weight's, BF16 for FP32)."""
     if weight.dtype not in (torch.bfloat16, torch.float16, torch.float32):
         raise EpError(-8, f"source dtype {weight.dtype}")
-    if weight.numel() == 0:
-        raise EpError(-1, "weight must not be empty")
+    if not weight.is_cuda or weight.dim() != 2 or weight.numel() == 0:
+        raise EpError(-1, "weight must be a non-empty 2-D CUDA tensor")
     if group not in INT4_GROUPS:
         raise EpError(-1, f"group must be one of {INT4_GROUPS}, not {group}")
     if dtype is None:
         dtype = torch.bfloat16 if weight.dtype == torch.float32 else weight.dtype
-    if dtype not in (torch.bfloat16, torch.float16):
+    if dtype not in _INT4_DTYPES:
         raise EpError(-1, f"scales are BF16 or FP16, not {dtype}")
-    if not weight.is_cuda or weight.dim() != 2:
-        raise EpError(-1, "weight must be a 2-D CUDA tensor")
-    with _Launch(weight, stream) as s:
-        w, ld = _rows(weight.detach(), "weight")
-        n, k = w.shape
-        codes = torch.empty((n, (k + 31) // 32 * 16), dtype=torch.uint8, device=w.device)
-        scales = torch.empty((n, -(-k // group)), dtype=dtype, device=w.device)
-        rc = lib().ep_int4_quantize(w.data_ptr(), CODE_OF[w.dtype], n, k, ld, group, codes.data_ptr(),
-                                    scales.data_ptr(), CODE_OF[dtype], s)
+    if _elsewhere(weight, stream):
+        with _made_current(weight, stream):
+            return int4_quantize(weight, group, dtype)
+    w, ld = _rows(weight)
+    n, k = w.shape
+    codes = w.new_empty((n, (k + 31) // 32 * 16), dtype=torch.uint8)
+    scales = w.new_empty((n, -(-k // group)), dtype=dtype)
+    rc = lib().ep_int4_quantize(w.data_ptr(), CODE_OF[w.dtype], n, k, ld, group, codes.data_ptr(), scales.data_ptr(),
+                                CODE_OF[dtype], _raw_stream(w.device.index))
     if rc != 0:
         raise EpError(rc, "ep_int4_quantize")
     return codes, scales
@@ -594,10 +587,12 @@ def int4_dequantize(codes, scales, in_features, group=128, out=None, stream=None
     if scales is None:
         raise EpError(-1, "scales are needed")
     n = _int4_weight(codes, scales, in_features, group)
-    with _Launch(codes, stream) as s:
-        out = _output(out, (n, in_features), scales.dtype, codes)
-        rc = lib().ep_int4_dequantize(codes.data_ptr(), scales.data_ptr(), CODE_OF[scales.dtype], n, in_features, group,
-                                      out.data_ptr(), s)
+    if _elsewhere(codes, stream):
+        with _made_current(codes, stream):
+            return int4_dequantize(codes, scales, in_features, group, out)
+    out = _output(out, codes, (n, in_features), scales.dtype)
+    rc = lib().ep_int4_dequantize(codes.data_ptr(), scales.data_ptr(), CODE_OF[scales.dtype], n, in_features, group,
+                                  out.data_ptr(), _raw_stream(codes.device.index))
     if rc != 0:
         raise EpError(rc, "ep_int4_dequantize")
     return out
@@ -607,21 +602,23 @@ def int4_linear(x, codes, scales, group=128, bias=None, out=None, status=None, s
     """Y = X W^T (+ bias) with a 4-bit group-scaled W (ep_int4_linear).  ``x``: CUDA (m, in_features) of the
     scales' dtype, any m, rows any distance apart; ``codes``, ``scales``: from ``int4_quantize``.  Returns
     the contiguous (m, out_features) output."""
-    if x.dim() != 2:
-        raise EpError(-1, "x must be a 2-D CUDA tensor")
-    k = x.shape[1]
+    if x.dim() != 2 or scales is None:
+        raise EpError(-1, "x must be a 2-D CUDA tensor, and scales are needed")
+    m, k = x.shape
     n = _int4_weight(codes, scales, k, group)
-    if x.dtype != scales.dtype or x.device != codes.device:
+    dtype, device = x.dtype, x.device
+    if dtype != scales.dtype or device != codes.device:
         raise EpError(-1, f"x must be {scales.dtype} on {codes.device}, as the scales are")
-    if bias is not None and (bias.dtype != x.dtype or bias.device != x.device or tuple(bias.shape) != (n,)
-                             or not bias.is_contiguous()):
-        raise EpError(-1, f"bias must be {n} contiguous {x.dtype} elements on {x.device}")
-    with _Launch(x, stream) as s:
-        x, ld = _rows(x, "x")
-        out = _output(out, (x.shape[0], n), x.dtype, x)
-        rc = lib().ep_int4_linear(codes.data_ptr(), scales.data_ptr(), n, k, group, CODE_OF[x.dtype], x.data_ptr(),
-                                  x.shape[0], ld, None if bias is None else bias.data_ptr(), out.data_ptr(),
-                                  _status(status, x), s)
+    if bias is not None and (bias.dtype != dtype or bias.device != device or bias.shape != (n,) or not bias.is_contiguous()):
+        raise EpError(-1, f"bias must be {n} contiguous {dtype} elements on {device}")
+    if _elsewhere(x, stream):
+        with _made_current(x, stream):
+            return int4_linear(x, codes, scales, group, bias, out, status)
+    x, ld = _rows(x)
+    out = _output(out, x, (m, n), dtype)
+    rc = lib().ep_int4_linear(codes.data_ptr(), scales.data_ptr(), n, k, group, CODE_OF[dtype], x.data_ptr(), m, ld,
+                              None if bias is None else bias.data_ptr(), out.data_ptr(), _status(status, x),
+                              _raw_stream(device.index))
     if rc != 0:
         raise EpError(rc, "ep_int4_linear")
     return out
@@ -633,13 +630,16 @@ def int4_linear_dx(dy, codes, scales, in_features, group=128, out=None, status=N
     if scales is None:
         raise EpError(-1, "scales are needed")
     n = _int4_weight(codes, scales, in_features, group)
-    if dy.dtype != scales.dtype or dy.device != codes.device:
-        raise EpError(-1, f"dy must be {scales.dtype} on {codes.device}, as the scales are")
-    with _Launch(codes, stream) as s:
-        dy, ld = _rows(dy, "dy", n)
-        out = _output(out, (dy.shape[0], in_features), dy.dtype, dy)
-        rc = lib().ep_int4_linear_dx(codes.data_ptr(), scales.data_ptr(), n, in_features, group, CODE_OF[dy.dtype],
-                                     dy.data_ptr(), dy.shape[0], ld, out.data_ptr(), _status(status, dy), s)
+    if dy.dim() != 2 or dy.shape[1] != n or dy.dtype != scales.dtype or dy.device != codes.device:
+        raise EpError(-1, f"dy must be (m, {n}) of {scales.dtype} on {codes.device}, as the scales are")
+    if _elsewhere(dy, stream):
+        with _made_current(dy, stream):
+            return int4_linear_dx(dy, codes, scales, in_features, group, out, status)
+    dy, ld = _rows(dy)
+    m = dy.shape[0]
+    out = _output(out, dy, (m, in_features), dy.dtype)
+    rc = lib().ep_int4_linear_dx(codes.data_ptr(), scales.data_ptr(), n, in_features, group, CODE_OF[dy.dtype],
+                                 dy.data_ptr(), m, ld, out.data_ptr(), _status(status, dy), _raw_stream(dy.device.index))
     if rc != 0:
         raise EpError(rc, "ep_int4_linear_dx")
     return out
@@ -650,26 +650,31 @@ def act8_pack(x, stream=None):
     (ep_act8_pack): codes int8 (m, ceil(features / 16) * 16), scales fp32 (m, ceil(features / 128))."""
     if x.dtype not in (torch.bfloat16, torch.float16, torch.float32):
         raise EpError(-8, f"source dtype {x.dtype}")
-    if x.dim() != 2 or x.shape[1] < 1 or not x.is_cuda:
+    if not x.is_cuda or x.dim() != 2 or x.shape[1] < 1:
         raise EpError(-1, "x must be a 2-D CUDA tensor with at least one feature")
-    with _Launch(x, stream) as s:
-        x, ld = _rows(x.detach(), "x")
-        m, k = x.shape
-        codes = torch.empty((m, (k + 15) // 16 * 16), dtype=torch.int8, device=x.device)
-        scales = torch.empty((m, -(-k // ACT8_GROUP)), dtype=torch.float32, device=x.device)
-        rc = lib().ep_act8_pack(x.data_ptr(), CODE_OF[x.dtype], m, k, ld, codes.data_ptr(), scales.data_ptr(), s)
+    if _elsewhere(x, stream):
+        with _made_current(x, stream):
+            return act8_pack(x)
+    x, ld = _rows(x)
+    m, k = x.shape
+    codes = x.new_empty((m, (k + 15) // 16 * 16), dtype=torch.int8)
+    scales = x.new_empty((m, -(-k // ACT8_GROUP)), dtype=torch.float32)
+    rc = lib().ep_act8_pack(x.data_ptr(), CODE_OF[x.dtype], m, k, ld, codes.data_ptr(), scales.data_ptr(),
+                            _raw_stream(x.device.index))
     if rc != 0:
         raise EpError(rc, "ep_act8_pack")
     return codes, scales
 
 
 def _act8(codes, scales, features):
-    if features < 1 or codes.dtype != torch.int8 or codes.dim() != 2 or codes.shape[1] != (features + 15) // 16 * 16 \
-            or not codes.is_contiguous() or not codes.is_cuda:
-        raise EpError(-1, f"checkpoint codes must be contiguous CUDA int8 rows of {(features + 15) // 16 * 16} bytes")
-    if scales.dtype != torch.float32 or tuple(scales.shape) != (codes.shape[0], -(-features // ACT8_GROUP)) \
+    row = (features + 15) // 16 * 16
+    if features < 1 or not codes.is_cuda or codes.dtype != torch.int8 or codes.dim() != 2 or codes.shape[1] != row \
+            or not codes.is_contiguous():
+        raise EpError(-1, f"checkpoint codes must be contiguous CUDA int8 rows of {row} bytes")
+    if scales.dtype != torch.float32 or scales.shape != (codes.shape[0], -(-features // ACT8_GROUP)) \
             or not scales.is_contiguous() or scales.device != codes.device:
-        raise EpError(-1, f"checkpoint scales must be contiguous fp32 of shape {(codes.shape[0], -(-features // ACT8_GROUP))}")
+        raise EpError(-1, "checkpoint scales must be contiguous fp32 of shape "
+                          f"{(codes.shape[0], -(-features // ACT8_GROUP))}")
 
 
 def act8_unpack(codes, scales, features, dtype=torch.bfloat16, out=None, stream=None):
@@ -677,10 +682,13 @@ def act8_unpack(codes, scales, features, dtype=torch.bfloat16, out=None, stream=
     _act8(codes, scales, features)
     if dtype not in (torch.bfloat16, torch.float16, torch.float32):
         raise EpError(-8, f"output dtype {dtype}")
-    with _Launch(codes, stream) as s:
-        out = _output(out, (codes.shape[0], features), dtype, codes)
-        rc = lib().ep_act8_unpack(codes.data_ptr(), scales.data_ptr(), codes.shape[0], features, out.data_ptr(),
-                                  CODE_OF[dtype], s)
+    if _elsewhere(codes, stream):
+        with _made_current(codes, stream):
+            return act8_unpack(codes, scales, features, dtype, out)
+    m = codes.shape[0]
+    out = _output(out, codes, (m, features), dtype)
+    rc = lib().ep_act8_unpack(codes.data_ptr(), scales.data_ptr(), m, features, out.data_ptr(), CODE_OF[dtype],
+                              _raw_stream(codes.device.index))
     if rc != 0:
         raise EpError(rc, "ep_act8_unpack")
     return out
@@ -692,17 +700,19 @@ def int4_scale_grad(dy, act_codes, act_scales, codes, in_features, group=128, ou
     Returns (out_features, ceil(in_features / group)) in dy's dtype."""
     n = _int4_weight(codes, None, in_features, group)
     _act8(act_codes, act_scales, in_features)
-    if dy.dtype not in (torch.bfloat16, torch.float16):
-        raise EpError(-1, f"dy must be BF16 or FP16, not {dy.dtype}")
-    if dy.device != codes.device or act_codes.device != codes.device or dy.dim() != 2 \
-            or dy.shape[0] != act_codes.shape[0]:
+    if dy.dtype not in _INT4_DTYPES or dy.dim() != 2 or dy.shape[1] != n:
+        raise EpError(-1, f"dy must be (m, {n}) of BF16 or FP16")
+    m = dy.shape[0]
+    if dy.device != codes.device or act_codes.device != codes.device or m != act_codes.shape[0]:
         raise EpError(-1, "dy, the checkpoint and the codes must be of the same tokens on one device")
-    with _Launch(codes, stream) as s:
-        dy, ld = _rows(dy, "dy", n)
-        out = _output(out, (n, -(-in_features // group)), dy.dtype, dy)
-        rc = lib().ep_int4_scale_grad(dy.data_ptr(), ld, act_codes.data_ptr(), act_scales.data_ptr(), dy.shape[0],
-                                      codes.data_ptr(), n, in_features, group, CODE_OF[dy.dtype], out.data_ptr(),
-                                      _status(status, dy), s)
+    if _elsewhere(dy, stream):
+        with _made_current(dy, stream):
+            return int4_scale_grad(dy, act_codes, act_scales, codes, in_features, group, out, status)
+    dy, ld = _rows(dy)
+    out = _output(out, dy, (n, -(-in_features // group)), dy.dtype)
+    rc = lib().ep_int4_scale_grad(dy.data_ptr(), ld, act_codes.data_ptr(), act_scales.data_ptr(), m, codes.data_ptr(), n,
+                                  in_features, group, CODE_OF[dy.dtype], out.data_ptr(), _status(status, dy),
+                                  _raw_stream(dy.device.index))
     if rc != 0:
         raise EpError(rc, "ep_int4_scale_grad")
     return out
