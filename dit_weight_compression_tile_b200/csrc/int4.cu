@@ -3,7 +3,7 @@
 // element once: HBM bounds them.
 #include <algorithm>
 
-#include "int4.cuh"
+#include "int4_gemm.cuh"
 
 namespace ep {
 namespace {
@@ -45,33 +45,152 @@ __device__ __forceinline__ uint32_t group_top(const float (&v)[8], int lanes) {
     return u;
 }
 
-// Checkpoint: 16 lanes hold one group of 128 features, eight each.  Scale a = max / 127 (rounded; 1 where
-// that is 0, NaN where the group has a NaN or an infinity, whose codes are 0).
+// 16 elements of a row as they are stored (beyond `valid`: 0)
 template <typename T>
-__global__ void __launch_bounds__(256) act8_pack_kernel(const T *x, int64_t ldx, uint32_t k, uint32_t groups,
-                                                        int64_t total, int8_t *codes, float *scales, bool aligned) {
-    const uint32_t l = threadIdx.x & 15u;
-    const int64_t unit = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 4;  // (token, group)
-    const bool in = unit < total;
-    const int64_t t = in ? unit / groups : 0;
-    const uint32_t g = uint32_t(in ? unit % groups : 0), k0 = g * kActGroup + l * 8;
-    float v[8];
-    load8<T>(x + t * ldx + k0, in ? int64_t(k) - k0 : 0, aligned, v);
-    const uint32_t top = group_top(v, 16);
-    float a = __fdiv_rn(__uint_as_float(top), 127.0f);
-    if (a == 0.0f) a = 1.0f;
-    const bool bad = top >= 0x7f800000u;
-    if (bad) a = __uint_as_float(0x7fffffffu);
-    const float unit_ = quotient_unit(a), s = a * unit_, inv = __frcp_rn(s);
-    uint32_t w[2] = {0u, 0u};
+struct Raw16 {
+    static constexpr int kWords = 4 * int(sizeof(T));
+    uint32_t w[kWords];
+    __device__ __forceinline__ void load(const T *p, int64_t valid, bool aligned) {
+        if (aligned && valid >= 16) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int c = bad ? 0 : quotient_code(v[i] * unit_, s, inv, 127.0f);
-        w[i / 4] |= (uint32_t(c) & 0xffu) << (8 * (i & 3));
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+                w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                if constexpr (sizeof(T) == 4) {
+                    w[i] = i < valid ? __ldg(reinterpret_cast<const uint32_t *>(p) + i) : 0u;
+                } else {
+                    const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+                    const uint32_t lo = 2 * i < valid ? __ldg(h + 2 * i) : 0u, hi = 2 * i + 1 < valid ? __ldg(h + 2 * i + 1) : 0u;
+                    w[i] = lo | (hi << 16);
+                }
+            }
+        }
     }
-    const int64_t row = act8_row_bytes(k);
-    if (in && k0 < row) *reinterpret_cast<uint2 *>(codes + t * row + k0) = make_uint2(w[0], w[1]);
-    if (in && l == 0) scales[unit] = a;
+    __device__ __forceinline__ float at(int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else return Elem<T>::f(uint16_t(w[i / 2] >> (16 * (i & 1))));
+    }
+    // the largest magnitude as fp32 bits, at least those of infinity where there is a NaN or an infinity:
+    // magnitudes order as integers, two at a time in 16-bit halves
+    __device__ __forceinline__ uint32_t top() const {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            if constexpr (sizeof(T) == 4) m = max(m, w[i] & 0x7fffffffu);
+            else m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+        }
+        if constexpr (sizeof(T) == 4) {
+            return m;
+        } else {
+            const uint32_t h = max(m & 0xffffu, m >> 16);
+            return __float_as_uint(Elem<T>::f(uint16_t(h))) | (h >= Elem<T>::kInf ? 0x7f800000u : 0u);
+        }
+    }
+};
+
+__device__ __forceinline__ float fma_sat(float a, float b, float c) {
+    float d;
+    asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// the bits of an fp32 mantissa below T's last place
+template <typename T>
+struct Below {
+    static constexpr uint32_t kBits = 0xffffu;
+};
+template <>
+struct Below<__half> {
+    static constexpr uint32_t kBits = 0x1fffu;
+};
+template <>
+struct Below<float> {
+    static constexpr uint32_t kBits = 0xffffffffu;  // (never 0: fp32 looks at each remainder)
+};
+
+struct PackArgs {
+    int64_t ldx, total;  // groups of all tokens
+    int64_t step_t;      // a CTA's next 32 groups are step_t tokens and step_g groups on
+    uint32_t k, groups, step_g;
+    bool aligned;
+};
+
+// Checkpoint: 8 lanes hold one group of 128 features, 16 each.  Scale a = max / 127 (rounded; 1 where
+// that is 0, NaN where the group has a NaN or an infinity, whose codes are 0).  q = x (1 / a) + 1.5 2^23 in
+// one fused multiply-add has the nearest integer in its low bits, wrong at most next to a half; the
+// remainder x - q a is exact (a multiple of a's last place, at most about a / 2) and says whether the next
+// integer is nearer: two saturated multiply-adds give the 0 or 1 to add and to subtract, on the pipe that
+// has room.  Groups where x / a can be an exact half (few: a has to be a short number; FP32: those that have
+// one) or a is tiny go by quotient_code.  With BF16 activations the quotients are fractions of small
+// numbers, and nine warps in ten have one next to a half: a slow path for all of those took 34 us for 4096
+// x 8192, comparing and selecting 26 us, rintf and a conversion for each element, on a half-rate pipe, 42 us.
+// CTAs walk over the groups with the next one's loads in flight.
+constexpr int kPackBlocks = 5;  // CTAs on an SM (4: the same; 6, with fewer registers: 27.6 us)
+template <typename T>
+__global__ void __launch_bounds__(256, kPackBlocks) act8_pack_kernel(const T *x, int8_t *codes, float *scales, const PackArgs p) {
+    const uint32_t l = threadIdx.x & 7u;
+    const int64_t row = act8_row_bytes(p.k);
+    int64_t unit = int64_t(blockIdx.x) * 32 + (threadIdx.x >> 3);  // (token, group)
+    int64_t t = uint32_t(unit) / p.groups;  // (the first groups' index has 32 bits)
+    uint32_t g = uint32_t(unit) % p.groups;
+    Raw16<T> next;
+    next.load(x + t * p.ldx + g * kActGroup + l * 16, unit < p.total ? int64_t(p.k) - int64_t(g * kActGroup + l * 16) : 0, p.aligned);
+    while (__any_sync(0xffffffffu, unit < p.total)) {
+        const Raw16<T> v = next;
+        const int64_t u0 = unit, t0 = t;
+        const uint32_t k0 = g * kActGroup + l * 16;
+        const bool in = unit < p.total;
+        unit += int64_t(gridDim.x) * 32;
+        t += p.step_t;
+        g += p.step_g;
+        if (g >= p.groups) g -= p.groups, ++t;
+        if (unit < p.total) next.load(x + t * p.ldx + g * kActGroup + l * 16, int64_t(p.k) - int64_t(g * kActGroup + l * 16), p.aligned);
+        uint32_t top = in ? v.top() : 0u;
+#pragma unroll
+        for (int d = 4; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+        float a = __fdiv_rn(__uint_as_float(top), 127.0f);
+        if (a == 0.0f) a = 1.0f;
+        const bool bad = top >= 0x7f800000u;
+        if (bad) a = __uint_as_float(0x7fffffffu);
+        // B = 2^(30 - e) for a in [2^e, 2^(e + 1)): the difference of two multiples of a's last place (halved)
+        // is 0 or at least 64 after it, so that the saturated product is 0 or 1
+        const uint32_t ab = __float_as_uint(a);
+        const float half = 0.5f * a, inv = __frcp_rn(a), unit_ = 12582912.0f;
+        const float B = __uint_as_float((284u << 23) - (ab & 0x7f800000u)), halfB = half * B;
+        // exact halves need a with no more digits than x has (an odd multiple of a / 2 has at least a's)
+        bool exact = bad || a < 0x1p-90f || !(ab & Below<T>::kBits);
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t b[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float f = v.at(4 * i + e), r = __fmaf_rn(f, inv, unit_);
+                const float rest = __fmaf_rn(unit_ - r, a, f);  // x - q a, exact
+                if (sizeof(T) == 4) exact |= fabsf(rest) == half;
+                b[e] = __float_as_uint(r + fma_sat(rest, B, -halfB) - fma_sat(-rest, B, -halfB));
+            }
+            w[i] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+        }
+        if (exact) {
+            const float up = quotient_unit(a), s = a * up, inv_s = __frcp_rn(s);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                w[i] = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int c = bad ? 0 : quotient_code(v.at(4 * i + e) * up, s, inv_s, 127.0f);
+                    w[i] |= (uint32_t(c) & 0xffu) << (8 * e);
+                }
+            }
+        }
+        if (in && k0 < row) *reinterpret_cast<uint4 *>(codes + t0 * row + k0) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (in && l == 0) scales[u0] = a;
+    }
 }
 
 // x = RNE(a c) in the output's type
@@ -170,21 +289,25 @@ extern "C" int ep_act8_pack(const void *d_x, int32_t dtype, int64_t m, int64_t k
         return EP_ERR_INVALID_ARG;
     const uint32_t groups = uint32_t((k + kActGroup - 1) / kActGroup);
     if (m > INT64_MAX / 64 / groups) return EP_ERR_UNSUPPORTED;
-    const int64_t total = m * groups;
-    unsigned grid;
-    if (!blocks_of(total * 16, &grid)) return EP_ERR_UNSUPPORTED;
-    const bool aligned = is16(d_x) && (m == 1 || ldx * elt % 16 == 0);
+    PackArgs p{};
+    p.ldx = ldx;
+    p.total = m * groups;
+    p.k = uint32_t(k);
+    p.groups = groups;
+    p.aligned = is16(d_x) && (m == 1 || ldx * elt % 16 == 0);
+    const int sms = device_sms();
+    if (sms < 1) return EP_ERR_CUDA;
+    const unsigned grid = unsigned(std::min<int64_t>((p.total + 31) / 32, int64_t(sms) * kPackBlocks));
+    p.step_t = int64_t(grid) * 32 / groups;
+    p.step_g = uint32_t(int64_t(grid) * 32 % groups);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     auto *c = static_cast<int8_t *>(d_codes);
     if (dtype == EP_BF16)
-        act8_pack_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16 *>(d_x), ldx, uint32_t(k), groups, total, c,
-                                              d_scales, aligned);
+        act8_pack_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16 *>(d_x), c, d_scales, p);
     else if (dtype == EP_FP16)
-        act8_pack_kernel<<<grid, 256, 0, s>>>(static_cast<const __half *>(d_x), ldx, uint32_t(k), groups, total, c,
-                                              d_scales, aligned);
+        act8_pack_kernel<<<grid, 256, 0, s>>>(static_cast<const __half *>(d_x), c, d_scales, p);
     else
-        act8_pack_kernel<<<grid, 256, 0, s>>>(static_cast<const float *>(d_x), ldx, uint32_t(k), groups, total, c,
-                                              d_scales, aligned);
+        act8_pack_kernel<<<grid, 256, 0, s>>>(static_cast<const float *>(d_x), c, d_scales, p);
     return cudaGetLastError() == cudaSuccess ? EP_OK : EP_ERR_CUDA;
 }
 

@@ -30,6 +30,7 @@ template <>
 struct Elem<__nv_bfloat16> {
     using Pair = __nv_bfloat162;
     static constexpr uint32_t kMagic = 0x43004300u;  // 128 + c for c < 128
+    static constexpr uint32_t kInf = 0x7f80u;
     __device__ static float f(uint16_t b) { return __uint_as_float(uint32_t(b) << 16); }
     __device__ static uint16_t bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 };
@@ -37,6 +38,7 @@ template <>
 struct Elem<__half> {
     using Pair = __half2;
     static constexpr uint32_t kMagic = 0x64006400u;  // 1024 + c for c < 1024
+    static constexpr uint32_t kInf = 0x7c00u;
     __device__ static float f(uint16_t b) { return __half2float(__ushort_as_half(b)); }
     __device__ static uint16_t bits(float v) { return __half_as_ushort(__float2half_rn(v)); }
 };

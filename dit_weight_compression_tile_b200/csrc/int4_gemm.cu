@@ -618,16 +618,6 @@ Int4Args args_of(int64_t n, int64_t k, int32_t group, const void *codes, const v
     a.act_groups = uint32_t((k + kActGroup - 1) / kActGroup);
     return a;
 }
-// the current device's SM count, looked up once per device
-int device_sms() {
-    static std::atomic<int> known[64];
-    int device = 0, sms = 0;
-    if (cudaGetDevice(&device) != cudaSuccess || device < 0 || device >= 64) return 0;
-    if ((sms = known[device].load()) == 0 &&
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) == cudaSuccess)
-        known[device].store(sms);
-    return sms;
-}
 constexpr size_t kSmemMost = 232448;
 
 // the launch: single or paired CTAs, tiles, the contraction's split, rings as deep as fit
@@ -723,6 +713,17 @@ using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t,
                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 }  // namespace
+
+// the current device's SM count, looked up once per device
+int device_sms() {
+    static std::atomic<int> known[64];
+    int device = 0, sms = 0;
+    if (cudaGetDevice(&device) != cudaSuccess || device < 0 || device >= 64) return 0;
+    if ((sms = known[device].load()) == 0 &&
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) == cudaSuccess)
+        known[device].store(sms);
+    return sms;
+}
 
 bool tensor_map(CUtensorMap *map, const void *base, CUtensorMapDataType type, uint32_t elt, uint64_t cols, uint64_t rows,
                 uint64_t pitch, uint32_t box_cols, uint32_t box_rows) {

@@ -21,6 +21,9 @@ struct Int4Args {
     uint32_t n, k, group, groups, words, act_groups;
 };
 
+// the current device's SM count (0: no device), looked up once per device
+int device_sms();
+
 constexpr int64_t kGemvTokens = 16;  // ep_int4_linear: up to here the weights' stream bounds it (int4_gemv.cu)
 int int4_gemv(const Int4Args &a, int32_t dtype, int sms, cudaStream_t s);
 
