@@ -489,6 +489,7 @@ def linear_fused(x, d_blob, info, tables, bias=None, out=None, work=None, status
 # ---------------------------------------------------------------- 4-bit weights with group scales
 INT4_GROUPS = (32, 64, 128)
 ACT8_GROUP = 128  # features per scale of an activation checkpoint
+INT4_STREAM_TOKENS = 16  # ep_int4_linear streams the weight for up to so many tokens (any rows will do)
 _INT4_DTYPES = (torch.bfloat16, torch.float16)
 
 
@@ -518,6 +519,18 @@ def _rows(t):
         t = t.detach().contiguous()
         ld = k
     return t, (ld if m > 1 else k)
+
+
+def _tiles(t):
+    """``_rows`` for the tensor-core products: those copy rows that begin on 16 bytes by TMA, others element
+    by element, so a large ``t`` that does not lie that way is first copied into rows that do (2048 x 8191
+    BF16: 3.3 ms against 0.2 ms; below 2^17 elements the copy costs more than it saves)"""
+    t, ld = _rows(t)
+    if (ld % 8 or t.data_ptr() % 16) and t.numel() >= 1 << 17:
+        m, k = t.shape
+        ld = (k + 7) // 8 * 8
+        t = t.new_empty((m, ld))[:, :k].copy_(t.detach())
+    return t, ld
 
 
 def _int4_weight(codes, scales, in_features, group):
@@ -598,30 +611,95 @@ def int4_dequantize(codes, scales, in_features, group=128, out=None, stream=None
     return out
 
 
+def _int4_linear_check(x, codes, scales, group, bias):
+    """checks the arguments of a forward; returns out_features"""
+    if x.dim() != 2 or scales is None:
+        raise EpError(-1, "x must be a 2-D CUDA tensor, and scales are needed")
+    n = _int4_weight(codes, scales, x.shape[1], group)
+    if x.dtype != scales.dtype or x.device != codes.device:
+        raise EpError(-1, f"x must be {scales.dtype} on {codes.device}, as the scales are")
+    if bias is not None and (bias.dtype != x.dtype or bias.device != x.device or bias.shape != (n,)
+                             or not bias.is_contiguous()):
+        raise EpError(-1, f"bias must be {n} contiguous {x.dtype} elements on {x.device}")
+    return n
+
+
+# The calls themselves, on checked arguments with the device and stream current
+def _launch_linear(x, codes, scales, n, group, bias, out, status):
+    m, k = x.shape
+    x, ld = _tiles(x) if m > INT4_STREAM_TOKENS else _rows(x)
+    rc = lib().ep_int4_linear(codes.data_ptr(), scales.data_ptr(), n, k, group, CODE_OF[x.dtype], x.data_ptr(), m, ld,
+                              None if bias is None else bias.data_ptr(), out.data_ptr(), status,
+                              _raw_stream(x.device.index))
+    if rc != 0:
+        raise EpError(rc, "ep_int4_linear")
+    return out
+
+
+def _launch_dx(dy, ld, codes, scales, k, group, out, status):
+    m, n = dy.shape
+    rc = lib().ep_int4_linear_dx(codes.data_ptr(), scales.data_ptr(), n, k, group, CODE_OF[dy.dtype], dy.data_ptr(), m, ld,
+                                 out.data_ptr(), status, _raw_stream(dy.device.index))
+    if rc != 0:
+        raise EpError(rc, "ep_int4_linear_dx")
+    return out
+
+
+def _launch_pack(x):
+    m, k = x.shape
+    codes = x.new_empty((m, (k + 15) // 16 * 16), dtype=torch.int8)
+    scales = x.new_empty((m, -(-k // ACT8_GROUP)), dtype=torch.float32)
+    x, ld = _rows(x)
+    rc = lib().ep_act8_pack(x.data_ptr(), CODE_OF[x.dtype], m, k, ld, codes.data_ptr(), scales.data_ptr(),
+                            _raw_stream(x.device.index))
+    if rc != 0:
+        raise EpError(rc, "ep_act8_pack")
+    return codes, scales
+
+
+def _launch_scale_grad(dy, ld, act_codes, act_scales, codes, k, group, out, status):
+    m, n = dy.shape
+    rc = lib().ep_int4_scale_grad(dy.data_ptr(), ld, act_codes.data_ptr(), act_scales.data_ptr(), m, codes.data_ptr(), n, k,
+                                  group, CODE_OF[dy.dtype], out.data_ptr(), status, _raw_stream(dy.device.index))
+    if rc != 0:
+        raise EpError(rc, "ep_int4_scale_grad")
+    return out
+
+
+def int4_layer_forward(x, codes, scales, group, bias, checkpoint):
+    """``int4_linear`` and, with ``checkpoint``, ``act8_pack`` of its input, checked once: (y, act_codes,
+    act_scales), the last two None without"""
+    n = _int4_linear_check(x, codes, scales, group, bias)
+    if _elsewhere(x, None):
+        with _made_current(x, None):
+            return int4_layer_forward(x, codes, scales, group, bias, checkpoint)
+    y = _launch_linear(x, codes, scales, n, group, bias, x.new_empty((x.shape[0], n)), None)
+    return (y, *_launch_pack(x)) if checkpoint else (y, None, None)
+
+
+def int4_layer_backward(dy, act_codes, act_scales, codes, scales, in_features, group, input_grad, scale_grad):
+    """the gradients (dx, ds) that are asked for (None otherwise) of ``int4_layer_forward``'s y, from what it
+    was given and gave: these are not checked again"""
+    if _elsewhere(dy, None):
+        with _made_current(dy, None):
+            return int4_layer_backward(dy, act_codes, act_scales, codes, scales, in_features, group, input_grad, scale_grad)
+    dy, ld = _tiles(dy)
+    dx = _launch_dx(dy, ld, codes, scales, in_features, group, dy.new_empty((dy.shape[0], in_features)), None) \
+        if input_grad else None
+    ds = _launch_scale_grad(dy, ld, act_codes, act_scales, codes, in_features, group, dy.new_empty(scales.shape), None) \
+        if scale_grad else None
+    return dx, ds
+
+
 def int4_linear(x, codes, scales, group=128, bias=None, out=None, status=None, stream=None):
     """Y = X W^T (+ bias) with a 4-bit group-scaled W (ep_int4_linear).  ``x``: CUDA (m, in_features) of the
     scales' dtype, any m, rows any distance apart; ``codes``, ``scales``: from ``int4_quantize``.  Returns
     the contiguous (m, out_features) output."""
-    if x.dim() != 2 or scales is None:
-        raise EpError(-1, "x must be a 2-D CUDA tensor, and scales are needed")
-    m, k = x.shape
-    n = _int4_weight(codes, scales, k, group)
-    dtype, device = x.dtype, x.device
-    if dtype != scales.dtype or device != codes.device:
-        raise EpError(-1, f"x must be {scales.dtype} on {codes.device}, as the scales are")
-    if bias is not None and (bias.dtype != dtype or bias.device != device or bias.shape != (n,) or not bias.is_contiguous()):
-        raise EpError(-1, f"bias must be {n} contiguous {dtype} elements on {device}")
+    n = _int4_linear_check(x, codes, scales, group, bias)
     if _elsewhere(x, stream):
         with _made_current(x, stream):
             return int4_linear(x, codes, scales, group, bias, out, status)
-    x, ld = _rows(x)
-    out = _output(out, x, (m, n), dtype)
-    rc = lib().ep_int4_linear(codes.data_ptr(), scales.data_ptr(), n, k, group, CODE_OF[dtype], x.data_ptr(), m, ld,
-                              None if bias is None else bias.data_ptr(), out.data_ptr(), _status(status, x),
-                              _raw_stream(device.index))
-    if rc != 0:
-        raise EpError(rc, "ep_int4_linear")
-    return out
+    return _launch_linear(x, codes, scales, n, group, bias, _output(out, x, (x.shape[0], n), x.dtype), _status(status, x))
 
 
 def int4_linear_dx(dy, codes, scales, in_features, group=128, out=None, status=None, stream=None):
@@ -635,14 +713,9 @@ def int4_linear_dx(dy, codes, scales, in_features, group=128, out=None, status=N
     if _elsewhere(dy, stream):
         with _made_current(dy, stream):
             return int4_linear_dx(dy, codes, scales, in_features, group, out, status)
-    dy, ld = _rows(dy)
-    m = dy.shape[0]
-    out = _output(out, dy, (m, in_features), dy.dtype)
-    rc = lib().ep_int4_linear_dx(codes.data_ptr(), scales.data_ptr(), n, in_features, group, CODE_OF[dy.dtype],
-                                 dy.data_ptr(), m, ld, out.data_ptr(), _status(status, dy), _raw_stream(dy.device.index))
-    if rc != 0:
-        raise EpError(rc, "ep_int4_linear_dx")
-    return out
+    dy, ld = _tiles(dy)
+    return _launch_dx(dy, ld, codes, scales, in_features, group, _output(out, dy, (dy.shape[0], in_features), dy.dtype),
+                      _status(status, dy))
 
 
 def act8_pack(x, stream=None):
@@ -655,15 +728,7 @@ def act8_pack(x, stream=None):
     if _elsewhere(x, stream):
         with _made_current(x, stream):
             return act8_pack(x)
-    x, ld = _rows(x)
-    m, k = x.shape
-    codes = x.new_empty((m, (k + 15) // 16 * 16), dtype=torch.int8)
-    scales = x.new_empty((m, -(-k // ACT8_GROUP)), dtype=torch.float32)
-    rc = lib().ep_act8_pack(x.data_ptr(), CODE_OF[x.dtype], m, k, ld, codes.data_ptr(), scales.data_ptr(),
-                            _raw_stream(x.device.index))
-    if rc != 0:
-        raise EpError(rc, "ep_act8_pack")
-    return codes, scales
+    return _launch_pack(x)
 
 
 def _act8(codes, scales, features):
@@ -702,17 +767,11 @@ def int4_scale_grad(dy, act_codes, act_scales, codes, in_features, group=128, ou
     _act8(act_codes, act_scales, in_features)
     if dy.dtype not in _INT4_DTYPES or dy.dim() != 2 or dy.shape[1] != n:
         raise EpError(-1, f"dy must be (m, {n}) of BF16 or FP16")
-    m = dy.shape[0]
-    if dy.device != codes.device or act_codes.device != codes.device or m != act_codes.shape[0]:
+    if dy.device != codes.device or act_codes.device != codes.device or dy.shape[0] != act_codes.shape[0]:
         raise EpError(-1, "dy, the checkpoint and the codes must be of the same tokens on one device")
     if _elsewhere(dy, stream):
         with _made_current(dy, stream):
             return int4_scale_grad(dy, act_codes, act_scales, codes, in_features, group, out, status)
-    dy, ld = _rows(dy)
-    out = _output(out, dy, (n, -(-in_features // group)), dy.dtype)
-    rc = lib().ep_int4_scale_grad(dy.data_ptr(), ld, act_codes.data_ptr(), act_scales.data_ptr(), m, codes.data_ptr(), n,
-                                  in_features, group, CODE_OF[dy.dtype], out.data_ptr(), _status(status, dy),
-                                  _raw_stream(dy.device.index))
-    if rc != 0:
-        raise EpError(rc, "ep_int4_scale_grad")
-    return out
+    dy, ld = _tiles(dy)
+    return _launch_scale_grad(dy, ld, act_codes, act_scales, codes, in_features, group,
+                              _output(out, dy, (n, -(-in_features // group)), dy.dtype), _status(status, dy))

@@ -278,7 +278,10 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
                 const uint16_t *row = a.scales + int64_t(o) * a.groups;
                 scale[0] = scale[1] = 0u;
                 if (o < a.n && k < a.k) scale[0] = ldg_now16(row + (k >> group_bits));
-                if (o < a.n && k + 32 < a.k) scale[1] = ldg_now16(row + ((k + 32) >> group_bits));
+                if (a.group > 32)
+                    scale[1] = scale[0];  // one load for the row's 64 inputs: every lane's is a line of its own
+                else if (o < a.n && k + 32 < a.k)
+                    scale[1] = ldg_now16(row + ((k + 32) >> group_bits));
             }
         };
         Walk mine{walker, 0};  // this group's next step
@@ -520,7 +523,6 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
         __syncwarp();
     } else {
         // ---- the dense operand through registers: 16-byte chunks of 8 elements, each checked
-        const uint32_t rows = P == kScaleGrad ? 64 : p.bn, boxes = P == kScaleGrad ? 2 : 1;
         const uint32_t cols_all = P == kForward ? a.k : a.n;
         Ring stage;
         for (uint32_t tile = walker; tile < p.tiles && !err; tile += walkers) {
@@ -532,26 +534,36 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
                     break;
                 }
                 const uint32_t dst = base + stage.at * stage_bytes + kQuantBytes;
-                for (uint32_t e = threadIdx.x - 32 * kDenseWarp0; e < boxes * rows * 8; e += 32 * kLoadWarps) {
-                    const uint32_t c = e & 7u, r = (e >> 3) % rows, box = (e >> 3) / rows;
-                    const int64_t t = (P == kScaleGrad ? 64 * int64_t(step) : b0) + r;
-                    const uint32_t col = (P == kScaleGrad ? uint32_t(b0) + 64 * box : 64 * step) + 8 * c;
-                    uint32_t v[4] = {0u, 0u, 0u, 0u};
-                    if (t < a.m && col < cols_all) {
+                // four chunks of a thread at a time, their loads in flight together
+                const uint32_t chunks = p.dense_bytes / 16, first = threadIdx.x - 32 * kDenseWarp0;
+                for (uint32_t e0 = first; e0 < chunks; e0 += 4 * 32 * kLoadWarps) {
+                    uint32_t v[4][4];
+#pragma unroll
+                    for (uint32_t u = 0; u < 4; ++u) {
+                        const uint32_t e = e0 + u * 32 * kLoadWarps, c = e & 7u;
+                        const uint32_t r = P == kScaleGrad ? (e >> 3) & 63u : e >> 3, box = P == kScaleGrad ? e >> 9 : 0u;
+                        const int64_t t = (P == kScaleGrad ? 64 * int64_t(step) : b0) + r;
+                        const uint32_t col = (P == kScaleGrad ? uint32_t(b0) + 64 * box : 64 * step) + 8 * c;
                         const uint16_t *src = a.x + t * a.ldx + col;
+                        v[u][0] = v[u][1] = v[u][2] = v[u][3] = 0u;
+                        if (e >= chunks || t >= a.m || col >= cols_all) continue;
                         if (p.dense_align >= 4 && col + 8 <= cols_all) {
 #pragma unroll
-                            for (uint32_t h = 0; h < 4; ++h) v[h] = __ldg(reinterpret_cast<const uint32_t *>(src) + h);
+                            for (uint32_t h = 0; h < 4; ++h) v[u][h] = __ldg(reinterpret_cast<const uint32_t *>(src) + h);
                         } else {
 #pragma unroll
                             for (uint32_t h = 0; h < 4; ++h) {
                                 const uint32_t lo = col + 2 * h < cols_all ? __ldg(src + 2 * h) : 0u;
                                 const uint32_t hi = col + 2 * h + 1 < cols_all ? __ldg(src + 2 * h + 1) : 0u;
-                                v[h] = lo | (hi << 16);
+                                v[u][h] = lo | (hi << 16);
                             }
                         }
                     }
-                    sts128(dst + 8192 * box + 128 * r + 16 * (c ^ (r & 7u)), v);
+#pragma unroll
+                    for (uint32_t u = 0; u < 4; ++u) {
+                        const uint32_t e = e0 + u * 32 * kLoadWarps, row = e >> 3;  // 128-byte rows, boxes of 64
+                        if (e < chunks) sts128(dst + 128 * row + 16 * ((e & 7u) ^ (row & 7u)), v[u]);
+                    }
                 }
                 fence_proxy_async();
                 __syncwarp();

@@ -254,22 +254,21 @@ class _Int4GroupLinear(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, codes, scales, bias, group):
-        k = x.shape[-1]
-        x2 = x.reshape(-1, k)
-        y = B.int4_linear(x2, codes, scales, group=group, bias=bias)
-        act = B.act8_pack(x2) if ctx.needs_input_grad[2] else (None, None)
-        ctx.save_for_backward(codes, scales, *act)
+        x2 = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
+        y, act_codes, act_scales = B.int4_layer_forward(x2, codes, scales, group, bias, ctx.needs_input_grad[2])
+        ctx.save_for_backward(codes, scales, act_codes, act_scales)
         ctx.group, ctx.x_shape = group, x.shape
-        return y.reshape(*x.shape[:-1], codes.shape[0])
+        return y if x.dim() == 2 else y.reshape(*x.shape[:-1], codes.shape[0])
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
         codes, scales, act_codes, act_scales = ctx.saved_tensors
-        k, dy2 = ctx.x_shape[-1], dy.reshape(-1, codes.shape[0])
         need_x, _, need_s, need_b, _ = ctx.needs_input_grad
-        dx = B.int4_linear_dx(dy2, codes, scales, k, group=ctx.group).reshape(ctx.x_shape) if need_x else None
-        ds = B.int4_scale_grad(dy2, act_codes, act_scales, codes, k, group=ctx.group) if need_s else None
+        dy2 = dy if dy.dim() == 2 else dy.reshape(-1, codes.shape[0])
+        dx, ds = B.int4_layer_backward(dy2, act_codes, act_scales, codes, scales, ctx.x_shape[-1], ctx.group, need_x, need_s)
+        if dx is not None and dy.dim() != 2:
+            dx = dx.reshape(ctx.x_shape)
         db = dy2.sum(0, dtype=torch.float32).to(dy.dtype) if need_b else None
         return dx, None, ds, db, None
 
