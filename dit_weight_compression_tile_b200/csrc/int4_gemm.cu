@@ -28,7 +28,8 @@ enum Product { kForward, kInputGrad, kScaleGrad };
 // first CTA's, for both), warp 21 copies the quantized operand's bytes, warp 22 the dense operand (x or
 // dy) by TMA, or warps 22..25 through registers where it is not 16-byte aligned.
 // Rings in shared memory, running on over the tiles:
-//   raw    the quantized operand's bytes, by TMA, slots of four steps (scale gradient: one)
+//   raw    the quantized operand's bytes, by TMA, slots of four steps, one for each group of four expansion
+//          warps (passing a slot costs a group 400 cycles, a seventh of its work on a step)
 //   stage  one step's operands: 16 KB expanded (16-bit), and the dense tile (up to 256 or, scale gradient,
 //          twice 64 rows of 128 bytes), both rows of 64 elements with the 128-byte swizzle
 // The expanded operand's rows follow the stored codes (64 consecutive inputs of one output feature or
@@ -54,10 +55,10 @@ struct MmaArgs {
     uint32_t dense_align;  // 4 or 2 bytes, where the dense operand is not copied by TMA
 };
 
+constexpr uint32_t kSlotSteps = 4;  // steps of a raw slot: one for each group of expansion warps
 template <int P>
 struct Shape {
-    static constexpr uint32_t kSlotSteps = P == kScaleGrad ? 1 : 4;
-    static constexpr uint32_t kRawBytes = P == kScaleGrad ? 8192 : 16384;
+    static constexpr uint32_t kRawBytes = P == kScaleGrad ? 32768 : 16384;
 };
 
 // shared-memory matrix descriptor, 128-byte swizzle: rows of 128 bytes, 8-row groups 1024 bytes apart.
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
     int4_mma_kernel(const __grid_constant__ MmaArgs p) {
     static_assert(TMA || !PAIR, "a pair copies its dense operand by TMA");
     extern __shared__ __align__(1024) uint8_t smem[];
-    constexpr uint32_t kSlotSteps = Shape<P>::kSlotSteps, kRawBytes = Shape<P>::kRawBytes, kWide = PAIR ? 256 : 128;
+    constexpr uint32_t kRawBytes = Shape<P>::kRawBytes, kWide = PAIR ? 256 : 128;
     const Int4Args &a = p.a;
     // (the shuffle tells the compiler that the role is the warp's: its loops' values then stay in uniform
     // registers, which the matrix instructions take their operands from)
@@ -264,31 +265,50 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
         const uint32_t group = warp >> 2, r = 32 * (warp & 3u) + lane, cc = r >> 6;
         const uint32_t group_bits = 31 - __clz(a.group);
         uint32_t scale[2];
-        // the thread's scales in a step (0 where there is none), read one step ahead
-        auto load_scales = [&](const Walk &w) {
-            if (w.tile >= p.tiles) return;
-            const uint32_t a0 = quant0(w.tile), step = step_lo + w.i;
+        // the thread's scales in a step (0 where there is none), read one step ahead.  What only a new tile
+        // changes is kept: recomputed each step, its division and products cost as much as the expansion
+        const uint16_t *scale_row = nullptr;  // of the tile: row r's (forward), or its first row's, at its first k
+        const float *act_row = nullptr;
+        uint32_t scale_k = 0;                 // first k of the thread's 64 (input gradient)
+        bool scale_in = false;
+        auto enter_tile = [&](uint32_t tile) {
+            if (tile >= p.tiles) return;
+            const uint32_t a0 = quant0(tile);
             if constexpr (P == kScaleGrad) {
-                const uint32_t t = 64 * step + (r & 63u);
-                scale[0] = 0u;
-                if (t < a.m && a0 < a.k) scale[0] = ldg_now32(a.act_scales + int64_t(t) * a.act_groups + a0 / 128);
+                act_row = a.act_scales + int64_t(64 * step_lo + (r & 63u)) * a.act_groups + a0 / 128;
+                scale_in = a0 < a.k;
+            } else if constexpr (P == kForward) {
+                scale_in = a0 + r < a.n;
+                scale_row = a.scales + int64_t(a0 + r) * a.groups;
             } else {
-                const uint32_t o = P == kForward ? a0 + r : 64 * step + (r & 63u);
-                const uint32_t k = P == kForward ? 64 * step : a0 + 64 * cc;
-                const uint16_t *row = a.scales + int64_t(o) * a.groups;
-                scale[0] = scale[1] = 0u;
-                if (o < a.n && k < a.k) scale[0] = ldg_now16(row + (k >> group_bits));
-                if (a.group > 32)
-                    scale[1] = scale[0];  // one load for the row's 64 inputs: every lane's is a line of its own
-                else if (o < a.n && k + 32 < a.k)
-                    scale[1] = ldg_now16(row + ((k + 32) >> group_bits));
+                scale_k = a0 + 64 * cc;
+                scale_in = scale_k < a.k;
+                scale_row = a.scales + int64_t(64 * step_lo + (r & 63u)) * a.groups + (scale_k >> group_bits);
+            }
+        };
+        auto load_scales = [&](uint32_t i) {  // step i of the tile entered last
+            scale[0] = scale[1] = 0u;
+            if constexpr (P == kScaleGrad) {
+                if (scale_in && 64 * (step_lo + i) + (r & 63u) < a.m) scale[0] = ldg_now32(act_row + int64_t(64 * i) * a.act_groups);
+            } else {
+                const uint32_t k = P == kForward ? 64 * (step_lo + i) : scale_k;
+                const uint16_t *at = P == kForward ? scale_row + (k >> group_bits) : scale_row + int64_t(64 * i) * a.groups;
+                if (scale_in && (P == kForward || 64 * (step_lo + i) + (r & 63u) < a.n)) {
+                    scale[0] = ldg_now16(at);
+                    if (a.group == 32) {
+                        if (k + 32 < a.k) scale[1] = ldg_now16(at + 1);
+                    } else {
+                        scale[1] = scale[0];  // one load for the row's 64 inputs: every lane's is a line of its own
+                    }
+                }
             }
         };
         Walk mine{walker, 0};  // this group's next step
         mine.advance(group, steps, walkers);
         Ring stage, raw;
         stage.advance(group, p.stages);
-        load_scales(mine);
+        enter_tile(mine.tile);
+        if (mine.tile < p.tiles) load_scales(mine.i);
         // every group passes every slot, in order, and frees it, whether it has a step there or not: none is
         // ever further ahead of another than the ring is long, so no turn is taken for another
         for (Walk at{walker, 0}; at.tile < p.tiles; raw.advance(1, p.raws)) {
@@ -306,8 +326,10 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
                 continue;
             }
             const uint32_t now[2] = {scale[0], scale[1]};
+            const uint32_t tile = mine.tile;
             mine.advance(kGroups, steps, walkers);
-            load_scales(mine);
+            if (mine.tile != tile) enter_tile(mine.tile);
+            if (mine.tile < p.tiles) load_scales(mine.i);
             const uint32_t src = raw0 + raw.at * kRawBytes;
             uint32_t out[8][4];
             if constexpr (P == kScaleGrad) {
@@ -486,7 +508,7 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
                     else if constexpr (P == kInputGrad)
                         tma_load(dst, &p.raw, a0 / 2, 256 * slot, bar);
                     else
-                        tma_load(dst, &p.raw, a0, 64 * slot, bar);
+                        tma_load(dst, &p.raw, a0, 256 * slot, bar);
                 }
             }
             // no copy is in flight when the CTA ends: the last use of each buffer
@@ -639,7 +661,7 @@ int launch_mma(const Int4Args &a, int sms, cudaStream_t s) {
     p.a = a;
     const int64_t contraction = P == kForward ? a.k : P == kInputGrad ? int64_t(a.n) : a.m;
     p.steps = uint32_t((contraction + 63) / 64);
-    p.slots = (p.steps + Shape<P>::kSlotSteps - 1) / Shape<P>::kSlotSteps;
+    p.slots = (p.steps + kSlotSteps - 1) / kSlotSteps;
     const uint64_t dense_cols = P == kForward ? a.k : a.n;
     const int64_t ld = a.m > 1 ? a.ldx : int64_t((dense_cols + 7) / 8 * 8);
     const bool tma = !misaligned(a.x, 16) && ld % 8 == 0 && ld < (int64_t(1) << 38) && a.m <= 0x7fffffff;
@@ -664,11 +686,15 @@ int launch_mma(const Int4Args &a, int sms, cudaStream_t s) {
     p.tiles_b = uint32_t(tiles_b);
     uint32_t splits = 1;
     if (!pair && p.tiles < uint32_t(sms))
-        splits = std::max(1u, std::min({8u, sms / p.tiles, p.slots / (P == kScaleGrad ? 4u : 1u)}));
+        splits = std::max(1u, std::min({8u, sms / p.tiles, p.slots}));
     const uint32_t stage = kQuantBytes + p.dense_bytes, raw = Shape<P>::kRawBytes;
-    p.raws = P == kScaleGrad ? 4 : 2;
-    p.stages = std::min<uint32_t>(kMaxStages, uint32_t((kSmemMost - kBarBytes - p.raws * raw) / stage));
-    p.raws = std::min<uint32_t>(kMaxRaws, uint32_t((kSmemMost - kBarBytes - p.stages * stage) / raw));
+    // 64 KB of raw slots where that leaves five stages, otherwise two slots and as many stages as fit
+    // (2048 x 8192 x 8192 forward, paired: 4 slots and 5 stages 187 us, 2 and 6 195 us)
+    const uint32_t room = uint32_t(kSmemMost - kBarBytes);
+    p.raws = 65536 / raw;
+    if (room < p.raws * raw + 5 * stage) p.raws = 2;
+    p.stages = std::min<uint32_t>(kMaxStages, (room - p.raws * raw) / stage);
+    p.raws = std::min<uint32_t>(kMaxRaws, (room - p.stages * stage) / raw);
     // a group waits for the matrix instructions that read its stage last; it has seen those of the turn
     // before done only if the ring holds a step of every group
     if (p.stages < kGroups) return EP_ERR_UNSUPPORTED;
@@ -683,7 +709,7 @@ int launch_mma(const Int4Args &a, int sms, cudaStream_t s) {
     const uint64_t pitch = P == kScaleGrad ? uint64_t(act8_row_bytes(a.k)) : uint64_t(a.words) * 4;
     const void *quant = P == kScaleGrad ? static_cast<const void *>(a.act) : static_cast<const void *>(a.codes);
     if (!tensor_map(&p.raw, quant, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, pitch, P == kScaleGrad ? uint64_t(a.m) : a.n, pitch,
-                    P == kInputGrad ? 64 : 128, P == kForward ? 128 : P == kInputGrad ? 256 : 64))
+                    P == kInputGrad ? 64 : 128, P == kForward ? 128 : 256))
         return EP_ERR_CUDA;
     if (tma && !tensor_map(&p.dense, a.x, dt, 2, dense_cols, uint64_t(a.m), uint64_t(ld) * 2, 64,
                            P == kScaleGrad ? 64 : p.dense_bytes / 128))
