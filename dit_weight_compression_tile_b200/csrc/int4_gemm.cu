@@ -202,12 +202,12 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
     const uint32_t stage_bytes = kQuantBytes + p.dense_bytes;
     const uint32_t raw0 = base + p.stages * stage_bytes, bars = raw0 + p.raws * kRawBytes;
     auto full = [&](uint32_t i) { return bars + 8 * i; };  // both operands of a stage
-    auto stage_free = [&](uint32_t i) { return bars + 128 + 8 * i; };
-    auto raw_full = [&](uint32_t i) { return bars + 192 + 8 * i; };
-    auto raw_free = [&](uint32_t i) { return bars + 256 + 8 * i; };
-    auto acc_full = [&](uint32_t i) { return bars + 320 + 8 * i; };
-    auto acc_free = [&](uint32_t i) { return bars + 336 + 8 * i; };
-    const uint32_t tmem_slot = bars + 352;
+    auto stage_free = [&](uint32_t i) { return bars + 64 + 8 * i; };
+    auto raw_full = [&](uint32_t i) { return bars + 128 + 8 * i; };
+    auto raw_free = [&](uint32_t i) { return bars + 192 + 8 * i; };
+    auto acc_full = [&](uint32_t i) { return bars + 256 + 8 * i; };
+    auto acc_free = [&](uint32_t i) { return bars + 272 + 8 * i; };
+    const uint32_t tmem_slot = bars + 288;
     // the walkers over tiles are CTAs or pairs; `half` is this CTA's place in its pair
     const uint32_t half = PAIR ? blockIdx.x & 1u : 0u, walker = PAIR ? blockIdx.x / 2 : blockIdx.x;
     const uint32_t walkers = PAIR ? gridDim.x / 2 : gridDim.x;
@@ -295,11 +295,9 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
                 const uint16_t *at = P == kForward ? scale_row + (k >> group_bits) : scale_row + int64_t(64 * i) * a.groups;
                 if (scale_in && (P == kForward || 64 * (step_lo + i) + (r & 63u) < a.n)) {
                     scale[0] = ldg_now16(at);
-                    if (a.group == 32) {
-                        if (k + 32 < a.k) scale[1] = ldg_now16(at + 1);
-                    } else {
-                        scale[1] = scale[0];  // one load for the row's 64 inputs: every lane's is a line of its own
-                    }
+                    // one load for groups of 64 and more: every lane's is a line of its own.  Inputs beyond the last
+                    // have codes of 0, which stand for -8: they get the scale 0, which no scale's range can spoil
+                    if (k + 32 < a.k) scale[1] = a.group == 32 ? ldg_now16(at + 1) : scale[0];
                 }
             }
         };
@@ -391,7 +389,10 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
         for (uint32_t tile = walker; tile < p.tiles; tile += walkers, acc.advance(1, 2)) {
             const uint32_t a0 = row0(tile);
             const int64_t b0 = col0(tile);
-            if (!mbar_wait(acc_full(acc.at), acc.phase)) {
+            // a whole tile's wait: its limit grows with the contraction
+            bool ready = false;
+            for (uint32_t i = 0; i <= steps / 1024 && !ready; ++i) ready = mbar_wait(acc_full(acc.at), acc.phase);
+            if (!ready) {
                 err = EP_DEC_TIMEOUT;
                 break;
             }

@@ -423,6 +423,101 @@ def test_nan_and_infinity_propagate(m):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("m", [2, 20, 300])
+@pytest.mark.parametrize("k", [70, 96, 128])
+def test_large_scales_do_not_spoil_the_padding(m, k):
+    """fp16 scales whose -8 s would overflow, with codes that do not: the inputs beyond k add nothing"""
+    n, group = 40, 32
+    rng = np.random.default_rng(k)
+    q = rng.integers(-7, 8, (n, k))
+    s = torch.full((n, -(-k // group)), 9000.0, dtype=HF)
+    x = torch.from_numpy(rng.normal(size=(m, k)) * 2.0 ** -8).to(HF)
+    ref, mag, sub = forward_ref(x, q, s, group, None)
+    check(B.int4_linear(x.cuda(), store(q).cuda(), s.cuda(), group=group), ref, mag, sub, k, HF)
+    dy = torch.from_numpy(rng.normal(size=(m, n)) * 2.0 ** -8).to(HF)
+    w, d = q * per_input(s, group, k), dy.double().numpy()
+    check(B.int4_linear_dx(dy.cuda(), store(q).cuda(), s.cuda(), k, group=group), d @ w, np.abs(d) @ np.abs(w),
+          np.abs(d).sum(1, keepdims=True), n, HF)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("amount", [1e-3, 1e-6, 3e4])
+def test_scale_grad_of_small_and_large_activations(amount):
+    """fp16 gradients on checkpoints whose scales an fp16 would not hold"""
+    m, n, k, group = 100, 72, 264, 64
+    q, codes, _, x = case(n, k, group, HF, 6, m)
+    x = (x.double() / x.double().abs().max() * amount).float()
+    c, a = B.act8_pack(x.cuda())
+    dy = torch.from_numpy(np.random.default_rng(1).normal(size=(m, n)) * 2.0 ** -9).to(HF)
+    ds = B.int4_scale_grad(dy.cuda(), c, a, codes.cuda(), k, group=group)
+    check(ds, *scale_grad_ref(dy, c.cpu().numpy(), a.cpu().numpy(), q, k, group), m + group, HF)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k,group", [(300, 2100, 1031, 32), (40, 4100, 4099, 64)])
+def test_large_operands_off_16_bytes(m, n, k, group):
+    q, codes, s, x = case(n, k, group, BF, 9, m)
+    dy = torch.from_numpy(np.random.default_rng(3).normal(size=(m, n))).to(BF)
+    ref, mag, sub = forward_ref(x, q, s, group, None)
+    check(B.int4_linear(x.cuda(), codes.cuda(), s.cuda(), group=group), ref, mag, sub, k, BF)
+    odd = torch.zeros(m * n + 1, dtype=BF, device="cuda")[1:].view(m, n)  # rows of n elements off by one
+    odd.copy_(dy)
+    w, d = q * per_input(s, group, k), dy.double().numpy()
+    check(B.int4_linear_dx(odd, codes.cuda(), s.cuda(), k, group=group), d @ w, np.abs(d) @ np.abs(w),
+          np.abs(d).sum(1, keepdims=True), n, BF)
+    c, a = pack_ref(x)
+    ds = B.int4_scale_grad(odd, torch.from_numpy(c).cuda(), torch.from_numpy(a).cuda(), codes.cuda(), k, group=group)
+    check(ds, *scale_grad_ref(dy, c, a, q, k, group), m + group, BF)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,group", [(BF, 128), (HF, 32)])
+@pytest.mark.parametrize("m,n,k", [(2048, 4096, 4096), (700, 5120, 5000), (512, 1024, 8192)])
+def test_same_bits_on_every_call(m, n, k, dtype, group):
+    """large products many times over, each the same to the last bit (a copy taken for the one before it
+    shows here), and near the product of the reconstructed weight in fp32"""
+    torch.manual_seed(m)
+    w = torch.randn(n, k, device="cuda") * 0.02
+    codes, s = B.int4_quantize(w, group, dtype=dtype)
+    x, dy = torch.randn(m, k, device="cuda").to(dtype), (torch.randn(m, n, device="cuda") * 0.1).to(dtype)
+    act = B.act8_pack(x)
+    wd = B.int4_dequantize(codes, s, k, group).float()
+    calls = [lambda: B.int4_linear(x, codes, s, group=group), lambda: B.int4_linear_dx(dy, codes, s, k, group=group),
+             lambda: B.int4_scale_grad(dy, *act, codes, k, group=group)]
+    first = [c() for c in calls]
+    for _ in range(6):
+        for f, c in zip(first, calls):
+            assert torch.equal(f, c())
+    # bounds: u for each operand rounded, k 2^-23 for sums (twice: the comparison sums in fp32 too), u for the result
+    for got, a, b, terms in ((first[0], x.float(), wd.T, k), (first[1], dy.float(), wd, n)):
+        ref, mag = a @ b, a.abs() @ b.abs()
+        tol = (2 * U[dtype] + terms * 2.0 ** -22) * mag + U[dtype] * ref.abs() + 1e-6
+        assert bool(((got.float() - ref).abs() <= tol).all())
+
+
+@pytest.mark.gpu
+def test_from_another_thread():
+    """a thread that has made no CUDA call of its own"""
+    import threading
+    q, codes, s, x = case(96, 256, 64, BF, 4, 48)
+    xc, cc, sc = x.cuda(), codes.cuda(), s.cuda()
+    want, out, caught = B.int4_linear(xc, cc, sc, group=64), torch.zeros(48, 96, dtype=BF, device="cuda"), []
+    torch.cuda.synchronize()
+
+    def call():
+        try:
+            B.int4_linear(xc, cc, sc, group=64, out=out)
+        except Exception as e:  # noqa: BLE001
+            caught.append(e)
+
+    t = threading.Thread(target=call)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert not caught and torch.equal(out, want)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("m", [5, 24])
 def test_rows_beyond_32_bits(m):
     """rows so far apart that their offsets pass 2^31 elements"""
