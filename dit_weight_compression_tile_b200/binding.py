@@ -493,14 +493,16 @@ INT4_STREAM_TOKENS = 16  # ep_int4_linear streams the weight for up to so many t
 _INT4_DTYPES = (torch.bfloat16, torch.float16)
 
 
-# the current stream's handle without building a Stream object around it (1 us of a call of 10)
+# the current stream's handle without building a Stream object around it, and the current device without
+# a look at whether CUDA is up (with CUDA tensors in hand it is): 1.5 us of a call of 10
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _elsewhere(t, stream):
     """whether a call on ``t`` must first make a device or a stream current"""
-    return stream is not None or torch.cuda.current_device() != t.device.index
+    return stream is not None or _current_device() != t.device.index
 
 
 @contextlib.contextmanager
@@ -615,13 +617,21 @@ def _int4_linear_check(x, codes, scales, group, bias):
     """checks the arguments of a forward; returns out_features"""
     if x.dim() != 2 or scales is None:
         raise EpError(-1, "x must be a 2-D CUDA tensor, and scales are needed")
-    n = _int4_weight(codes, scales, x.shape[1], group)
-    if x.dtype != scales.dtype or x.device != codes.device:
+    k = x.shape[1]
+    dtype, device = x.dtype, x.device
+    if codes.dim() == 2 and k > 0 and group in INT4_GROUPS and dtype in _INT4_DTYPES and device.type == "cuda":
+        n = codes.shape[0]
+        if (n > 0 and codes.shape[1] == (k + 31) // 32 * 16 and codes.dtype == torch.uint8 and codes.device == device
+                and codes.is_contiguous() and scales.shape == (n, -(-k // group)) and scales.dtype == dtype
+                and scales.device == device and scales.is_contiguous()
+                and (bias is None or (bias.shape == (n,) and bias.dtype == dtype and bias.device == device
+                                      and bias.is_contiguous()))):
+            return n
+    # something is wrong: say what
+    n = _int4_weight(codes, scales, k, group)
+    if dtype != scales.dtype or device != codes.device:
         raise EpError(-1, f"x must be {scales.dtype} on {codes.device}, as the scales are")
-    if bias is not None and (bias.dtype != x.dtype or bias.device != x.device or bias.shape != (n,)
-                             or not bias.is_contiguous()):
-        raise EpError(-1, f"bias must be {n} contiguous {x.dtype} elements on {x.device}")
-    return n
+    raise EpError(-1, f"bias must be {n} contiguous {dtype} elements on {device}")
 
 
 # The calls themselves, on checked arguments with the device and stream current
@@ -657,37 +667,50 @@ def _launch_pack(x):
     return codes, scales
 
 
-def _launch_scale_grad(dy, ld, act_codes, act_scales, codes, k, group, out, status):
+def _launch_scale_grad(dy, ld, act_codes, act_scales, codes, k, group, out, status):  # (the checkpoint: addresses)
     m, n = dy.shape
-    rc = lib().ep_int4_scale_grad(dy.data_ptr(), ld, act_codes.data_ptr(), act_scales.data_ptr(), m, codes.data_ptr(), n, k,
-                                  group, CODE_OF[dy.dtype], out.data_ptr(), status, _raw_stream(dy.device.index))
+    rc = lib().ep_int4_scale_grad(dy.data_ptr(), ld, act_codes, act_scales, m, codes.data_ptr(), n, k, group,
+                                  CODE_OF[dy.dtype], out.data_ptr(), status, _raw_stream(dy.device.index))
     if rc != 0:
         raise EpError(rc, "ep_int4_scale_grad")
     return out
 
 
 def int4_layer_forward(x, codes, scales, group, bias, checkpoint):
-    """``int4_linear`` and, with ``checkpoint``, ``act8_pack`` of its input, checked once: (y, act_codes,
-    act_scales), the last two None without"""
+    """``int4_linear`` and, with ``checkpoint``, ``act8_pack`` of its input, checked once: (y, act), act one
+    int8 tensor with the checkpoint's codes and, from the next multiple of 16 bytes, its scales, or None"""
     n = _int4_linear_check(x, codes, scales, group, bias)
     if _elsewhere(x, None):
         with _made_current(x, None):
             return int4_layer_forward(x, codes, scales, group, bias, checkpoint)
-    y = _launch_linear(x, codes, scales, n, group, bias, x.new_empty((x.shape[0], n)), None)
-    return (y, *_launch_pack(x)) if checkpoint else (y, None, None)
+    m, k = x.shape
+    y = _launch_linear(x, codes, scales, n, group, bias, x.new_empty((m, n)), None)
+    if not checkpoint:
+        return y, None
+    size = m * ((k + 15) // 16 * 16)
+    act = x.new_empty(size + 4 * m * -(-k // ACT8_GROUP), dtype=torch.int8)
+    x, ld = _rows(x)
+    at = act.data_ptr()
+    rc = lib().ep_act8_pack(x.data_ptr(), CODE_OF[x.dtype], m, k, ld, at, at + size, _raw_stream(x.device.index))
+    if rc != 0:
+        raise EpError(rc, "ep_act8_pack")
+    return y, act
 
 
-def int4_layer_backward(dy, act_codes, act_scales, codes, scales, in_features, group, input_grad, scale_grad):
+def int4_layer_backward(dy, act, codes, scales, in_features, group, input_grad, scale_grad):
     """the gradients (dx, ds) that are asked for (None otherwise) of ``int4_layer_forward``'s y, from what it
     was given and gave: these are not checked again"""
     if _elsewhere(dy, None):
         with _made_current(dy, None):
-            return int4_layer_backward(dy, act_codes, act_scales, codes, scales, in_features, group, input_grad, scale_grad)
+            return int4_layer_backward(dy, act, codes, scales, in_features, group, input_grad, scale_grad)
     dy, ld = _tiles(dy)
-    dx = _launch_dx(dy, ld, codes, scales, in_features, group, dy.new_empty((dy.shape[0], in_features)), None) \
-        if input_grad else None
-    ds = _launch_scale_grad(dy, ld, act_codes, act_scales, codes, in_features, group, dy.new_empty(scales.shape), None) \
-        if scale_grad else None
+    dx = ds = None
+    if input_grad:
+        dx = _launch_dx(dy, ld, codes, scales, in_features, group, dy.new_empty((dy.shape[0], in_features)), None)
+    if scale_grad:
+        at = act.data_ptr()
+        ds = _launch_scale_grad(dy, ld, at, at + dy.shape[0] * ((in_features + 15) // 16 * 16), codes, in_features, group,
+                                dy.new_empty(scales.shape), None)
     return dx, ds
 
 
@@ -773,5 +796,5 @@ def int4_scale_grad(dy, act_codes, act_scales, codes, in_features, group=128, ou
         with _made_current(dy, stream):
             return int4_scale_grad(dy, act_codes, act_scales, codes, in_features, group, out, status)
     dy, ld = _tiles(dy)
-    return _launch_scale_grad(dy, ld, act_codes, act_scales, codes, in_features, group,
+    return _launch_scale_grad(dy, ld, act_codes.data_ptr(), act_scales.data_ptr(), codes, in_features, group,
                               _output(out, dy, (n, -(-in_features // group)), dy.dtype), _status(status, dy))

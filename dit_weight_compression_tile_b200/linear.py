@@ -255,18 +255,18 @@ class _Int4GroupLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, codes, scales, bias, group):
         x2 = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
-        y, act_codes, act_scales = B.int4_layer_forward(x2, codes, scales, group, bias, ctx.needs_input_grad[2])
-        ctx.save_for_backward(codes, scales, act_codes, act_scales)
+        y, act = B.int4_layer_forward(x2, codes, scales, group, bias, ctx.needs_input_grad[2])
+        ctx.save_for_backward(codes, scales, act)
         ctx.group, ctx.x_shape = group, x.shape
         return y if x.dim() == 2 else y.reshape(*x.shape[:-1], codes.shape[0])
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
-        codes, scales, act_codes, act_scales = ctx.saved_tensors
+        codes, scales, act = ctx.saved_tensors
         need_x, _, need_s, need_b, _ = ctx.needs_input_grad
         dy2 = dy if dy.dim() == 2 else dy.reshape(-1, codes.shape[0])
-        dx, ds = B.int4_layer_backward(dy2, act_codes, act_scales, codes, scales, ctx.x_shape[-1], ctx.group, need_x, need_s)
+        dx, ds = B.int4_layer_backward(dy2, act, codes, scales, ctx.x_shape[-1], ctx.group, need_x, need_s)
         if dx is not None and dy.dim() != 2:
             dx = dx.reshape(ctx.x_shape)
         db = dy2.sum(0, dtype=torch.float32).to(dy.dtype) if need_b else None
@@ -277,7 +277,8 @@ def int4_group_linear(x, codes, scales, bias=None, group=128):
     """y = x W^T (+ bias) for x (..., in_features) and a 4-bit group-scaled weight (``int4_quantize``),
     x, scales and bias of one type (BF16 or FP16).  Differentiable in x, scales and bias; the gradient of
     the scales is taken on the input's 8-bit checkpoint (``act8_pack``), about 1/254 of each group of 128
-    features' largest magnitude off at most per value."""
+    features' largest magnitude off at most per value.  (As with any such function: do not capture the
+    backward into a CUDA graph while an eager graph of the same leaves is alive.)"""
     if not torch.is_tensor(x) or x.dim() < 1:
         raise B.EpError(-1, "x must be a (..., in_features) tensor")
     return _Int4GroupLinear.apply(x, codes, scales, bias, group)
