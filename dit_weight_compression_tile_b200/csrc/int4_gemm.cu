@@ -389,6 +389,18 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
         for (uint32_t tile = walker; tile < p.tiles; tile += walkers, acc.advance(1, 2)) {
             const uint32_t a0 = row0(tile);
             const int64_t b0 = col0(tile);
+            // scale gradient: the lane's output feature o, and its codes of the tile (their loads under way while
+            // the tile's sums are; loaded as they are used they made a tile's output 4 us)
+            const uint32_t o = a0 + 32 * q + lane;
+            uint4 codes[P == kScaleGrad ? kWide / 32 : 1];
+            if constexpr (P == kScaleGrad) {
+                const uint4 *at = reinterpret_cast<const uint4 *>(a.codes + int64_t(min(o, a.n - 1)) * a.words + b0 / 8);
+#pragma unroll
+                for (uint32_t c = 0; c < kWide / 32; ++c)  // 32 inputs: 16 bytes
+                    codes[c] = uint32_t(b0) + 32 * c < 8 * a.words
+                                   ? __ldg(at + c)
+                                   : make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+            }
             // a whole tile's wait: its limit grows with the contraction
             bool ready = false;
             for (uint32_t i = 0; i <= steps / 1024 && !ready; ++i) ready = mbar_wait(acc_full(acc.at), acc.phase);
@@ -399,15 +411,12 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t from = tmem + ((32u * q) << 16) + acc.at * p.bn;
             if constexpr (P == kScaleGrad) {
-                // lane: output feature o; its row of D times its codes, summed over 32 inputs, then over a group
-                const uint32_t o = a0 + 32 * q + lane;
-                const uint4 *codes = reinterpret_cast<const uint4 *>(a.codes + int64_t(min(o, a.n - 1)) * a.words + b0 / 8);
+                // its row of D times its codes, summed over 32 inputs, then over a group
                 uint16_t *out = a.out + int64_t(o) * a.groups + b0 / a.group;
                 float sum = 0.0f;
-                for (uint32_t c = 0; c < kWide / 32; ++c) {  // 32 inputs: 16 bytes of codes
-                    const uint32_t k = uint32_t(b0) + 32 * c;
-                    const uint4 v = k < 8 * a.words ? __ldg(codes + c) : make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (uint32_t c = 0; c < kWide / 32; ++c) {
+                    const uint32_t w[4] = {codes[c].x, codes[c].y, codes[c].z, codes[c].w};
                     float s = 0.0f;
 #pragma unroll
                     for (uint32_t h = 0; h < 2; ++h) {
@@ -415,8 +424,9 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
                         tmem_load16(d, from + 32 * c + 16 * h);
 #pragma unroll
                         for (uint32_t e = 0; e < 16; ++e) {
+                            // (2^23 + the code, less 2^23 + 8: a conversion runs at an eighth of the rate)
                             const uint32_t in = e & 7u, code = (w[2 * h + e / 8] >> (4 * (in / 2) + 16 * (in & 1u))) & 15u;
-                            s = fmaf(__uint_as_float(d[e]), float(int(code) - 8), s);
+                            s = fmaf(__uint_as_float(d[e]), __uint_as_float(0x4b000000u | code) - 8388616.0f, s);
                         }
                     }
                     if (splits > 1) {
