@@ -678,8 +678,12 @@ int launch_mma(const Int4Args &a, int sms, cudaStream_t s) {
     const bool tma = !misaligned(a.x, 16) && ld % 8 == 0 && ld < (int64_t(1) << 38) && a.m <= 0x7fffffff;
     p.dense_align = !misaligned(a.x, 4) && ld % 2 == 0 ? 4 : 2;
     const uint64_t rows = P == kInputGrad ? a.k : a.n, cols = P == kScaleGrad ? a.k : uint64_t(a.m);
-    // pairs where their tiles (256 x 256) keep most SMs busy
-    const bool pair = tma && cols > 128 && ((rows + 255) / 256) * ((cols + 255) / 256) * 8 >= uint64_t(sms) * 3;
+    // pairs where their tiles (256 x 256) keep most SMs busy: from 3/8 of a tile per SM, a quarter in the
+    // scale gradient, whose single tiles are half as wide.  Measured, pairs against single CTAs with the
+    // contraction split: forward 512 x 4096 x 4096 (32 tiles) 31 us against 25, 1024 x 4096 x 4096 (64) 32
+    // against 33; scale gradient 2048 x 1024 x 1536 (24) 18.6 against 17.0, 2048 x 1536 x 2048 (48) 20 against 29
+    const uint64_t pair_tiles = ((rows + 255) / 256) * ((cols + 255) / 256);
+    const bool pair = tma && cols > 128 && pair_tiles * 8 >= uint64_t(sms) * (P == kScaleGrad ? 2 : 3);
     const uint64_t tiles_a = pair ? (rows + 255) / 256 : (rows + 127) / 128;
     uint64_t tiles_b;
     if (P == kScaleGrad) {
