@@ -98,19 +98,31 @@ __device__ __forceinline__ float fma_sat(float a, float b, float c) {
     return d;
 }
 
-// the bits of an fp32 mantissa below T's last place
+// Whether x / a can be an exact half that the first rounding does not already send to the even integer.  An
+// odd multiple of a / 2 has at least a's digits, so a must be no longer than x; a = m 2^e / 127 with m an integer of
+// x's length is an integer times 2^e, or periodic and as long as an fp32 can be; and for a power of two the
+// reciprocal and the rounding are exact.  BF16's m, below 256, leave 127 and 254: powers of two.
 template <typename T>
-struct Below {
-    static constexpr uint32_t kBits = 0xffffu;
-};
+constexpr bool kHalves = true;
 template <>
-struct Below<__half> {
-    static constexpr uint32_t kBits = 0x1fffu;
+constexpr bool kHalves<__nv_bfloat16> = false;
+
+// the exact way, for the groups that need it (a call: written in place it cost every group 4 us in 27)
+struct Slow16 {
+    float x[16];
+    uint32_t w[4];
 };
-template <>
-struct Below<float> {
-    static constexpr uint32_t kBits = 0xffffffffu;  // (never 0: fp32 looks at each remainder)
-};
+__device__ __noinline__ void act8_codes_slow(Slow16 *p, bool bad, float a) {
+    const float up = quotient_unit(a), s = a * up, inv = __frcp_rn(s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t w = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            w |= (uint32_t(bad ? 0 : quotient_code(p->x[4 * i + e] * up, s, inv, 127.0f)) & 0xffu) << (8 * e);
+        p->w[i] = w;
+    }
+}
 
 struct PackArgs {
     int64_t ldx, total;  // groups of all tokens
@@ -123,12 +135,12 @@ struct PackArgs {
 // that is 0, NaN where the group has a NaN or an infinity, whose codes are 0).  q = x (1 / a) + 1.5 2^23 in
 // one fused multiply-add has the nearest integer in its low bits, wrong at most next to a half; the
 // remainder x - q a is exact (a multiple of a's last place, at most about a / 2) and says whether the next
-// integer is nearer: two saturated multiply-adds give the 0 or 1 to add and to subtract, on the pipe that
-// has room.  Groups where x / a can be an exact half (few: a has to be a short number; FP32: those that have
-// one) or a is tiny go by quotient_code.  With BF16 activations the quotients are fractions of small
-// numbers, and nine warps in ten have one next to a half: a slow path for all of those took 34 us for 4096
-// x 8192, comparing and selecting 26 us, rintf and a conversion for each element, on a half-rate pipe, 42 us.
-// CTAs walk over the groups with the next one's loads in flight.
+// integer is nearer, or (kHalves) as near and even: two saturated multiply-adds give the 0 or 1 to add and to
+// subtract, on the pipe that has room.  Tiny a go by quotient_code.  With BF16 activations the quotients are
+// fractions of small numbers, and nine warps in ten have one next to a half: a slow path for all of those
+// took 34 us for 4096 x 8192, comparing and selecting 26 us, rintf and a conversion for each element, on a
+// half-rate pipe, 42 us.  Copying alone takes 16.3 us in this form: the instructions bound it.  CTAs walk over
+// the groups with the next one's loads in flight.
 constexpr int kPackBlocks = 5;  // CTAs on an SM (4: the same; 6, with fewer registers: 27.6 us)
 template <typename T>
 __global__ void __launch_bounds__(256, kPackBlocks) act8_pack_kernel(const T *x, int8_t *codes, float *scales, const PackArgs p) {
@@ -161,8 +173,7 @@ __global__ void __launch_bounds__(256, kPackBlocks) act8_pack_kernel(const T *x,
         const uint32_t ab = __float_as_uint(a);
         const float half = 0.5f * a, inv = __frcp_rn(a), unit_ = 12582912.0f;
         const float B = __uint_as_float((284u << 23) - (ab & 0x7f800000u)), halfB = half * B;
-        // exact halves need a with no more digits than x has (an odd multiple of a / 2 has at least a's)
-        bool exact = bad || a < 0x1p-90f || !(ab & Below<T>::kBits);
+        const bool exact = bad || a < 0x1p-90f;
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -171,22 +182,19 @@ __global__ void __launch_bounds__(256, kPackBlocks) act8_pack_kernel(const T *x,
             for (int e = 0; e < 4; ++e) {
                 const float f = v.at(4 * i + e), r = __fmaf_rn(f, inv, unit_);
                 const float rest = __fmaf_rn(unit_ - r, a, f);  // x - q a, exact
-                if (sizeof(T) == 4) exact |= fabsf(rest) == half;
-                b[e] = __float_as_uint(r + fma_sat(rest, B, -halfB) - fma_sat(-rest, B, -halfB));
+                // (an odd q gives way at half already: from half on, the sum is at least half a last place of halfB)
+                const float limit = kHalves<T> ? __uint_as_float(__float_as_uint(-halfB) - (__float_as_uint(r) & 1u)) : -halfB;
+                b[e] = __float_as_uint(r + fma_sat(rest, B, limit) - fma_sat(-rest, B, limit));
             }
             w[i] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
         }
         if (exact) {
-            const float up = quotient_unit(a), s = a * up, inv_s = __frcp_rn(s);
+            Slow16 slow;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                w[i] = 0;
+            for (int i = 0; i < 16; ++i) slow.x[i] = v.at(i);
+            act8_codes_slow(&slow, bad, a);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int c = bad ? 0 : quotient_code(v.at(4 * i + e) * up, s, inv_s, 127.0f);
-                    w[i] |= (uint32_t(c) & 0xffu) << (8 * e);
-                }
-            }
+            for (int i = 0; i < 4; ++i) w[i] = slow.w[i];
         }
         if (in && k0 < row) *reinterpret_cast<uint4 *>(codes + t0 * row + k0) = make_uint4(w[0], w[1], w[2], w[3]);
         if (in && l == 0) scales[u0] = a;
