@@ -288,7 +288,7 @@ constexpr int64_t kMaxDim = int64_t(1) << 30;
 extern "C" int ep_act8_pack(const void *d_x, int32_t dtype, int64_t m, int64_t k, int64_t ldx, void *d_codes,
                             float *d_scales, ep_stream_t stream) {
     using namespace ep;
-    if (m < 0 || k < 1 || k > kMaxDim || (m > 1 && ldx < k)) return EP_ERR_INVALID_ARG;
+    if (m < 0 || m > kMaxDim || k < 1 || k > kMaxDim || (m > 1 && ldx < k)) return EP_ERR_INVALID_ARG;
     if (dtype != EP_BF16 && dtype != EP_FP16 && dtype != EP_FP32) return EP_ERR_INVALID_ARG;
     if (m == 0) return EP_OK;
     const uint32_t elt = dtype == EP_FP32 ? 4 : 2;
@@ -322,7 +322,7 @@ extern "C" int ep_act8_pack(const void *d_x, int32_t dtype, int64_t m, int64_t k
 extern "C" int ep_act8_unpack(const void *d_codes, const float *d_scales, int64_t m, int64_t k, void *d_out,
                               int32_t dtype, ep_stream_t stream) {
     using namespace ep;
-    if (m < 0 || k < 1 || k > kMaxDim) return EP_ERR_INVALID_ARG;
+    if (m < 0 || m > kMaxDim || k < 1 || k > kMaxDim) return EP_ERR_INVALID_ARG;
     if (dtype != EP_BF16 && dtype != EP_FP16 && dtype != EP_FP32) return EP_ERR_INVALID_ARG;
     if (m == 0) return EP_OK;
     const uint32_t elt = dtype == EP_FP32 ? 4 : 2;

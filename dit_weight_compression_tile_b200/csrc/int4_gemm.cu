@@ -815,7 +815,7 @@ extern "C" int ep_int4_linear(const void *d_codes, const void *d_scales, int64_t
                               int32_t dtype, const void *d_x, int64_t m, int64_t ldx, const void *d_bias, void *d_y,
                               uint32_t *d_status, ep_stream_t stream) {
     using namespace ep;
-    if (!weight_ok(n, k, group, dtype) || m < 0 || (m > 1 && ldx < k)) return EP_ERR_INVALID_ARG;
+    if (!weight_ok(n, k, group, dtype) || m < 0 || m > kMaxDim || (m > 1 && ldx < k)) return EP_ERR_INVALID_ARG;
     if (m == 0) return EP_OK;
     if (!d_codes || !d_scales || !d_x || !d_y || misaligned(d_codes, 16) || misaligned(d_scales, 2) ||
         misaligned(d_x, 2) || misaligned(d_bias, 2) || misaligned(d_y, 2) || misaligned(d_status, 4))
@@ -837,7 +837,7 @@ extern "C" int ep_int4_linear_dx(const void *d_codes, const void *d_scales, int6
                                  int32_t dtype, const void *d_dy, int64_t m, int64_t lddy, void *d_dx,
                                  uint32_t *d_status, ep_stream_t stream) {
     using namespace ep;
-    if (!weight_ok(n, k, group, dtype) || m < 0 || (m > 1 && lddy < n)) return EP_ERR_INVALID_ARG;
+    if (!weight_ok(n, k, group, dtype) || m < 0 || m > kMaxDim || (m > 1 && lddy < n)) return EP_ERR_INVALID_ARG;
     if (m == 0) return EP_OK;
     if (!d_codes || !d_scales || !d_dy || !d_dx || misaligned(d_codes, 16) || misaligned(d_scales, 2) ||
         misaligned(d_dy, 2) || misaligned(d_dx, 2) || misaligned(d_status, 4))
@@ -857,7 +857,7 @@ extern "C" int ep_int4_scale_grad(const void *d_dy, int64_t lddy, const void *d_
                                   int64_t m, const void *d_codes, int64_t n, int64_t k, int32_t group, int32_t dtype,
                                   void *d_ds, uint32_t *d_status, ep_stream_t stream) {
     using namespace ep;
-    if (!weight_ok(n, k, group, dtype) || m < 0 || (m > 1 && lddy < n)) return EP_ERR_INVALID_ARG;
+    if (!weight_ok(n, k, group, dtype) || m < 0 || m > kMaxDim || (m > 1 && lddy < n)) return EP_ERR_INVALID_ARG;
     if (!d_codes || !d_ds || misaligned(d_codes, 16) || misaligned(d_ds, 2) || misaligned(d_status, 4))
         return EP_ERR_INVALID_ARG;
     if (m > 0 && (!d_dy || !d_act || !d_act_scales || misaligned(d_dy, 2) || misaligned(d_act, 16) ||

@@ -72,7 +72,8 @@ int ep_act8_unpack(const void *d_codes, const float *d_scales, int64_t m, int64_
 
 /* The gradient of every group scale from the output's gradient and the forward's checkpointed input:
  * ds[o, g] = sum over k in group g of q[o, k] sum_t dy[t, o] a[t, k / 128] c[t, k], n x ceil(k / group) of
- * dtype.  The weight gradient itself is never written. */
+ * dtype.  The weight gradient itself is never written.  dtype EP_FP16 holds a c in 16 bits too: activations
+ * beyond its range, which only an FP32 x has, make their groups' sums infinite or NaN. */
 int ep_int4_scale_grad(const void *d_dy, int64_t lddy, const void *d_act, const float *d_act_scales, int64_t m,
                        const void *d_codes, int64_t n, int64_t k, int32_t group, int32_t dtype, void *d_ds,
                        uint32_t *d_status, ep_stream_t stream);

@@ -139,6 +139,19 @@ def test_refused_before_any_launch():
     assert L.ep_int4_dequantize(FAKE, None, B.BF16, 4, 64, 32, FAKE, None) == -1
 
 
+def test_sizes_beyond_the_limit_are_refused():
+    L, big = B.lib(), 2 ** 30 + 1
+    for m in (big, 2 ** 40):
+        assert L.ep_int4_linear(FAKE, FAKE, 1, 32, 32, B.BF16, FAKE, m, 32, None, FAKE, None, None) == -1
+        assert L.ep_int4_linear_dx(FAKE, FAKE, 1, 32, 32, B.BF16, FAKE, m, 1, FAKE, None, None) == -1
+        assert L.ep_int4_scale_grad(FAKE, 1, FAKE, FAKE, m, FAKE, 1, 32, 32, B.BF16, FAKE, None, None) == -1
+        assert L.ep_act8_pack(FAKE, B.BF16, m, 32, 32, FAKE, FAKE, None) == -1
+        assert L.ep_act8_unpack(FAKE, FAKE, m, 32, FAKE, B.BF16, None) == -1
+    assert L.ep_act8_pack(FAKE, B.BF16, 1, big, big, FAKE, FAKE, None) == -1
+    assert L.ep_int4_quantize(FAKE, B.BF16, big, 32, 32, 32, FAKE, FAKE, B.BF16, None) == -1
+    assert L.ep_int4_dequantize(FAKE, FAKE, B.BF16, 1, big, 32, FAKE, None) == -1
+
+
 def test_binding_and_layer_refuse():
     q, codes, s, x = case(8, 64, 32, BF, 0, 3)
     for call in (lambda: B.int4_linear(x, codes, s, group=32), lambda: B.int4_quantize(x, 32), lambda: B.act8_pack(x),
