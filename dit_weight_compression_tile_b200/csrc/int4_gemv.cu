@@ -86,15 +86,43 @@ __device__ __forceinline__ uint4 ldg_stream(const void *p) {
     return v;
 }
 
-// the words and scales of one block of 128 inputs for a lane's 2 RG features
-template <uint32_t GPB, uint32_t RG>
-struct Block {
-    uint4 w[2 * RG];
-    uint16_t s[2 * RG][GPB];
+// A block's scales of one feature: as one load where rows of scales allow it (SVEC), one for each otherwise
+template <uint32_t GPB, bool SVEC>
+struct Scales {
+    uint16_t s[GPB];
+    __device__ __forceinline__ void load(const uint16_t *p) {
+#pragma unroll
+        for (uint32_t h = 0; h < GPB; ++h) s[h] = __ldg(p + h);
+    }
+    __device__ __forceinline__ uint16_t get(uint32_t h) const { return s[h]; }
+    __device__ __forceinline__ void set(uint32_t h, uint16_t v) { s[h] = v; }
+};
+template <uint32_t GPB>
+struct Scales<GPB, true> {
+    uint32_t s[GPB / 2];
+    __device__ __forceinline__ void load(const uint16_t *p) {
+        if constexpr (GPB == 2) {
+            s[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+        } else {
+            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
+            s[0] = v.x, s[1] = v.y;
+        }
+    }
+    __device__ __forceinline__ uint16_t get(uint32_t h) const { return uint16_t(s[h / 2] >> (16 * (h & 1u))); }
+    __device__ __forceinline__ void set(uint32_t h, uint16_t v) {
+        s[h / 2] = h & 1u ? (s[h / 2] & 0xffffu) | uint32_t(v) << 16 : (s[h / 2] & 0xffff0000u) | v;
+    }
 };
 
-// RG: 16-feature tiles of a warp; NT: 8-token tiles; VEC: x is read 16 bytes at a time
-template <typename T, uint32_t GPB, uint32_t NT, uint32_t RG, bool VEC>
+// the words and scales of one block of 128 inputs for a lane's 2 RG features
+template <uint32_t GPB, uint32_t RG, bool SVEC>
+struct Block {
+    uint4 w[2 * RG];
+    Scales<GPB, SVEC> s[2 * RG];
+};
+
+// RG: 16-feature tiles of a warp; NT: 8-token tiles; VEC: x is read 16 bytes at a time; SVEC: Scales
+template <typename T, uint32_t GPB, uint32_t NT, uint32_t RG, bool VEC, bool SVEC>
 __global__ void __launch_bounds__(256, 2) int4_gemv_kernel(const __grid_constant__ GemvArgs p) {
     constexpr uint32_t kTok = 8 * NT, kPerGroup = 8 / GPB, kDeep = 4 / RG;  // mma steps per group, blocks in flight
     __shared__ float part[kWarps][16 * RG][kTok + 1];
@@ -120,17 +148,16 @@ __global__ void __launch_bounds__(256, 2) int4_gemv_kernel(const __grid_constant
     for (uint32_t t = 0; t < NT; ++t) xp[t] = a.x + int64_t(min(8 * t + g, m - 1)) * a.ldx + 128 * b0;
 
     float total[RG][NT][4] = {};
-    auto load = [&](uint32_t ahead, Block<GPB, RG> &k) {  // a whole block, `ahead` of the current one
+    auto load = [&](uint32_t ahead, Block<GPB, RG, SVEC> &k) {  // a whole block, `ahead` of the current one
 #pragma unroll
         for (uint32_t i = 0; i < 2 * RG; ++i) {
             if (have[i]) {
                 k.w[i] = ldg_stream(wp[i] + 16 * ahead);
-#pragma unroll
-                for (uint32_t h = 0; h < GPB; ++h) k.s[i][h] = __ldg(sp[i] + ahead * GPB + h);
+                k.s[i].load(sp[i] + ahead * GPB);
             }
         }
     };
-    auto multiply = [&](Block<GPB, RG> &k, const uint32_t (&x)[NT][16]) {
+    auto multiply = [&](Block<GPB, RG, SVEC> &k, const uint32_t (&x)[NT][16]) {
         uint32_t w[2 * RG][4];
 #pragma unroll
         for (uint32_t i = 0; i < 2 * RG; ++i) {
@@ -160,7 +187,7 @@ __global__ void __launch_bounds__(256, 2) int4_gemv_kernel(const __grid_constant
             }
 #pragma unroll
             for (uint32_t r = 0; r < RG; ++r) {
-                const float fa = Elem<T>::f(k.s[2 * r][h]), fb = Elem<T>::f(k.s[2 * r + 1][h]);
+                const float fa = Elem<T>::f(k.s[2 * r].get(h)), fb = Elem<T>::f(k.s[2 * r + 1].get(h));
 #pragma unroll
                 for (uint32_t t = 0; t < NT; ++t) {
                     total[r][t][0] = fmaf(fa, acc[r][t][0], total[r][t][0]);
@@ -172,7 +199,7 @@ __global__ void __launch_bounds__(256, 2) int4_gemv_kernel(const __grid_constant
         }
     };
     // this lane's B fragments of a block: inputs lane_offset(h, c) .. of token g (and g + 8)
-    auto compute = [&](uint32_t ahead, Block<GPB, RG> &k) {
+    auto compute = [&](uint32_t ahead, Block<GPB, RG, SVEC> &k) {
         uint32_t x[NT][16];
 #pragma unroll
         for (uint32_t t = 0; t < NT; ++t)
@@ -185,17 +212,17 @@ __global__ void __launch_bounds__(256, 2) int4_gemv_kernel(const __grid_constant
             }
         multiply(k, x);
     };
-    const Block<GPB, RG> zero = [] {
-        Block<GPB, RG> z;
+    const Block<GPB, RG, SVEC> zero = [] {
+        Block<GPB, RG, SVEC> z;
         for (uint32_t i = 0; i < 2 * RG; ++i) {
             z.w[i] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-            for (uint32_t h = 0; h < GPB; ++h) z.s[i][h] = 0;
+            for (uint32_t h = 0; h < GPB; ++h) z.s[i].set(h, 0);
         }
         return z;
     }();
     // kDeep blocks' loads in flight, each turn multiplies the oldest and loads the next
     if (b0 < whole) {
-        Block<GPB, RG> k[kDeep];
+        Block<GPB, RG, SVEC> k[kDeep];
 #pragma unroll
         for (uint32_t i = 0; i < kDeep; ++i) {
             k[i] = zero;
@@ -217,14 +244,14 @@ __global__ void __launch_bounds__(256, 2) int4_gemv_kernel(const __grid_constant
     // the block that k ends in, and every block of an x that is not 16-byte aligned: each word, group and
     // input checked (beyond k: q = 0, x = 0)
     for (uint32_t b = max(b0, whole); b < b1; ++b) {
-        Block<GPB, RG> k = zero;
+        Block<GPB, RG, SVEC> k = zero;
 #pragma unroll
         for (uint32_t i = 0; i < 2 * RG; ++i) {
             const int64_t r = row0 + 8 * i + g;
             if (have[i] && 16 * b + 4 * c < a.words) k.w[i] = ldg_stream(a.codes + r * a.words + 16 * b + 4 * c);
 #pragma unroll
             for (uint32_t h = 0; h < GPB; ++h)
-                if (have[i] && b * GPB + h < a.groups) k.s[i][h] = __ldg(a.scales + r * a.groups + b * GPB + h);
+                if (have[i] && b * GPB + h < a.groups) k.s[i].set(h, __ldg(a.scales + r * a.groups + b * GPB + h));
         }
         uint32_t x[NT][16];
 #pragma unroll
@@ -273,21 +300,26 @@ __global__ void __launch_bounds__(256, 2) int4_gemv_kernel(const __grid_constant
     }
 }
 
-template <typename T, uint32_t NT, uint32_t RG, bool VEC>
+template <typename T, uint32_t GPB, uint32_t NT, uint32_t RG>
 int launch_gemv(const GemvArgs &p, unsigned grid, cudaStream_t s) {
-    const auto kern = p.a.group == 128 ? int4_gemv_kernel<T, 1, NT, RG, VEC>
-                      : p.a.group == 64 ? int4_gemv_kernel<T, 2, NT, RG, VEC>
-                                        : int4_gemv_kernel<T, 4, NT, RG, VEC>;
+    // (one scale a block is one load either way; without whole blocks none is made)
+    const bool svec = GPB > 1 && p.a.groups % GPB == 0 && (reinterpret_cast<uintptr_t>(p.a.scales) & (2 * GPB - 1)) == 0;
+    const auto kern = p.xvec != 16 ? int4_gemv_kernel<T, GPB, NT, RG, false, false>
+                      : svec       ? int4_gemv_kernel<T, GPB, NT, RG, true, (GPB > 1)>
+                                   : int4_gemv_kernel<T, GPB, NT, RG, true, false>;
     kern<<<grid, 32 * kWarps, 0, s>>>(p);
     return cudaGetLastError() == cudaSuccess ? EP_OK : EP_ERR_CUDA;
 }
+template <typename T, uint32_t NT, uint32_t RG>
+int launch_gemv_group(const GemvArgs &p, unsigned grid, cudaStream_t s) {
+    return p.a.group == 128  ? launch_gemv<T, 1, NT, RG>(p, grid, s)
+           : p.a.group == 64 ? launch_gemv<T, 2, NT, RG>(p, grid, s)
+                             : launch_gemv<T, 4, NT, RG>(p, grid, s);
+}
 template <typename T>
 int launch_gemv_for(const GemvArgs &p, uint32_t nt, uint32_t rg, unsigned grid, cudaStream_t s) {
-    const bool vec = p.xvec == 16;
-    if (nt == 1 && rg == 1) return vec ? launch_gemv<T, 1, 1, true>(p, grid, s) : launch_gemv<T, 1, 1, false>(p, grid, s);
-    if (nt == 1) return vec ? launch_gemv<T, 1, 2, true>(p, grid, s) : launch_gemv<T, 1, 2, false>(p, grid, s);
-    if (rg == 1) return vec ? launch_gemv<T, 2, 1, true>(p, grid, s) : launch_gemv<T, 2, 1, false>(p, grid, s);
-    return vec ? launch_gemv<T, 2, 2, true>(p, grid, s) : launch_gemv<T, 2, 2, false>(p, grid, s);
+    if (nt == 1) return rg == 1 ? launch_gemv_group<T, 1, 1>(p, grid, s) : launch_gemv_group<T, 1, 2>(p, grid, s);
+    return rg == 1 ? launch_gemv_group<T, 2, 1>(p, grid, s) : launch_gemv_group<T, 2, 2>(p, grid, s);
 }
 
 }  // namespace
