@@ -1,5 +1,9 @@
 // ep_int4_linear for few tokens (m <= kGemvTokens): every weight is read once from memory and multiplied
-// for all tokens, so HBM bounds it (0.5 bytes and 2 m flops per weight).
+// for all tokens (0.5 bytes and 2 m flops per weight: HBM's time is the floor).
+// Measured on a B200: 8192 x 28672, groups of 128, one token 29.7 us, 8 tokens 33.7, 16 tokens 48.6; groups
+// of 64 and 32, one token 35.0 and 38.3.  The stream alone takes 18.5 us at the copy rate and 20.8 us by these
+// loads: turning codes into operands (9 instructions for 8 weights) and x's passage through L1 are what is left
+// (issue slots 47 %, ALU pipe 53 %, L1 64 % busy).  1024 x 1024: 2.4 us, a launch.
 #include <algorithm>
 
 #include "int4_gemm.cuh"
@@ -7,28 +11,28 @@
 namespace ep {
 namespace {
 
-// A warp takes 16 output features and a range of inputs in blocks of 128: lane (g = lane / 4, c = lane % 4)
-// loads the 16 bytes of inputs 32 c .. 32 c + 31 of the block for features g and g + 8 (a quad reads 64
-// contiguous bytes), turns pairs of codes into exact 16-bit numbers (code_pairs) and feeds them to mma.m16n8k16 as A, with the tokens as B (8 per tile, absent
-// ones 0).  The inputs that one mma contracts may be any 16 as long as A and B agree, so a lane's B
-// fragments are contiguous inputs of its token, read as 16 bytes through L1.  Each group of inputs has
-// its own accumulation, scaled in fp32 by s and added to the total: q and x are exact, only sums round.
+// A warp takes RG tiles of 16 output features and a range of inputs in blocks of 128: lane (g = lane / 4,
+// c = lane % 4) loads the 16 bytes of inputs 32 c .. 32 c + 31 of the block for features g and g + 8 of a
+// tile (a quad reads 64 contiguous bytes), turns pairs of codes into exact 16-bit numbers (code_pairs) and
+// feeds them to mma.m16n8k16 as A, with the tokens as B (8 per tile, absent ones the last one's).  The inputs
+// that one mma contracts may be any 16 as long as A and B agree, so a lane's B fragments are contiguous inputs
+// of its token, read as 16 bytes through L1.  Each group of inputs has its own accumulation, scaled in fp32 by s
+// and added to the total: q and x are exact, only sums round.
 // Groups of 64 (32) inputs: the quad first exchanges words so that each mma stays within a group
-// (2 (4) shuffles per 16 bytes), after which lane c holds, of the block's group h, the inputs from
-// lane_offset(h, c), 32 / (128 / group) of them.
-// The tensor cores are the cheap way to the products (one instruction per 8 weights of a lane for up to
-// 8 tokens); what bounds the kernel is the stream of weights.
-template <uint32_t GPB>  // groups per block of 128 inputs
+// (2 (4) shuffles per 16 bytes), after which lane c holds, of the block's half (quarter) h, the inputs from
+// lane_offset(h, c), 16 (8) of them.
+// The tensor cores are the cheap way to the products: one instruction per 8 weights of a lane for up to 8 tokens.
+template <uint32_t X>  // parts of the block of 128 inputs
 __device__ __forceinline__ uint32_t lane_offset(uint32_t h, uint32_t c) {
-    if constexpr (GPB == 1) return 32 * c;
-    if constexpr (GPB == 2) return 64 * h + 32 * (c & 1u) + 16 * (c >> 1);
+    if constexpr (X == 1) return 32 * c;
+    if constexpr (X == 2) return 64 * h + 32 * (c & 1u) + 16 * (c >> 1);
     return 32 * h + 8 * c;
 }
 
-// the quad's words so that word GPB == 1: j, 2: 2 h + (0, 1), 4: h belongs to group h
-template <uint32_t GPB>
+// the quad's words so that word 2 h, 2 h + 1 (X == 2) or h (X == 4) belongs to part h
+template <uint32_t X>
 __device__ __forceinline__ void exchange(uint32_t (&w)[4], uint32_t c) {
-    if constexpr (GPB >= 2) {  // with the lane two away: it keeps the half of each chunk that c's bit 1 names
+    if constexpr (X >= 2) {  // with the lane two away: it keeps the half of each chunk that c's bit 1 names
         const bool up = c & 2u;
         const uint32_t a = __shfl_xor_sync(0xffffffffu, up ? w[0] : w[2], 2);
         const uint32_t b = __shfl_xor_sync(0xffffffffu, up ? w[1] : w[3], 2);
@@ -37,7 +41,7 @@ __device__ __forceinline__ void exchange(uint32_t (&w)[4], uint32_t c) {
         w[2] = up ? w[2] : a;
         w[3] = up ? w[3] : b;
     }
-    if constexpr (GPB == 4) {
+    if constexpr (X == 4) {
         // now w[0], w[1]: words (2 b1, 2 b1 + 1) of chunk b0; w[2], w[3]: of chunk 2 + b0 (c = 2 b1 + b0)
         const bool up = c & 1u;
         const uint32_t a = __shfl_xor_sync(0xffffffffu, up ? w[0] : w[1], 1);
@@ -77,6 +81,7 @@ struct GemvArgs {
 };
 
 constexpr uint32_t kWarps = 8;
+constexpr uint32_t ctas_on_sm(uint32_t rg) { return rg == 4 ? 1 : 2; }
 
 __device__ __forceinline__ uint4 ldg_stream(const void *p) {
     uint4 v;
@@ -123,8 +128,12 @@ struct Block {
 
 // RG: 16-feature tiles of a warp; NT: 8-token tiles; VEC: x is read 16 bytes at a time; SVEC: Scales
 template <typename T, uint32_t GPB, uint32_t NT, uint32_t RG, bool VEC, bool SVEC>
-__global__ void __launch_bounds__(256, 2) int4_gemv_kernel(const __grid_constant__ GemvArgs p) {
-    constexpr uint32_t kTok = 8 * NT, kPerGroup = 8 / GPB, kDeep = 4 / RG;  // mma steps per group, blocks in flight
+__global__ void __launch_bounds__(32 * kWarps, ctas_on_sm(RG)) int4_gemv_kernel(const __grid_constant__ GemvArgs p) {
+    constexpr uint32_t kTok = 8 * NT, kPerGroup = 8 / GPB, kDeep = RG == 1 && NT == 1 ? 4 : 2;  // mma steps per group, blocks in flight
+    // how far the quad's words are exchanged: for the groups, and for groups of 128 where it pays that the quad's
+    // reads of x then lie in one line of 128 bytes (16 tokens: 4096 x 11008 13.6 us against 17.4, but 8192 x 28672,
+    // with 64 features a warp, 51.4 against 48.8; 1 and 8 tokens there: 35.5 and 36.2 against 29.7 and 33.7)
+    constexpr uint32_t X = GPB == 1 && NT == 2 && RG == 1 ? 2 : GPB;
     __shared__ float part[kWarps][16 * RG][kTok + 1];
     const Int4Args &a = p.a;
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3u;
@@ -162,7 +171,7 @@ __global__ void __launch_bounds__(256, 2) int4_gemv_kernel(const __grid_constant
 #pragma unroll
         for (uint32_t i = 0; i < 2 * RG; ++i) {
             w[i][0] = k.w[i].x, w[i][1] = k.w[i].y, w[i][2] = k.w[i].z, w[i][3] = k.w[i].w;
-            exchange<GPB>(w[i], c);
+            exchange<X>(w[i], c);
         }
 #pragma unroll
         for (uint32_t h = 0; h < GPB; ++h) {
@@ -205,9 +214,8 @@ __global__ void __launch_bounds__(256, 2) int4_gemv_kernel(const __grid_constant
         for (uint32_t t = 0; t < NT; ++t)
 #pragma unroll
             for (uint32_t q = 0; q < 4; ++q) {
-                const uint4 r = __ldg(reinterpret_cast<const uint4 *>(xp[t] + lane_offset<GPB>(0, c) + 128 * ahead +
-                                                                      lane_offset<GPB>(q * GPB / 4, 0) +
-                                                                      8 * (q % (4 / GPB))));
+                const uint4 r = __ldg(reinterpret_cast<const uint4 *>(xp[t] + lane_offset<X>(0, c) + 128 * ahead +
+                                                                      lane_offset<X>(q * X / 4, 0) + 8 * (q % (4 / X))));
                 x[t][4 * q] = r.x, x[t][4 * q + 1] = r.y, x[t][4 * q + 2] = r.z, x[t][4 * q + 3] = r.w;
             }
         multiply(k, x);
@@ -259,7 +267,7 @@ __global__ void __launch_bounds__(256, 2) int4_gemv_kernel(const __grid_constant
             const uint16_t *row = a.x + int64_t(min(8 * t + g, m - 1)) * a.ldx;
 #pragma unroll
             for (uint32_t q = 0; q < 4; ++q) {
-                const uint32_t at = 128 * b + lane_offset<GPB>(q * GPB / 4, c) + 8 * (q % (4 / GPB));
+                const uint32_t at = 128 * b + lane_offset<X>(q * X / 4, c) + 8 * (q % (4 / X));
                 const uint16_t *src = row + at;
                 uint32_t *dst = &x[t][4 * q];
                 if (p.xvec >= 4 && at + 8 <= a.k) {
@@ -289,7 +297,7 @@ __global__ void __launch_bounds__(256, 2) int4_gemv_kernel(const __grid_constant
     __syncthreads();
     // each feature's slices in order, the bias, one rounding
     const uint32_t rows = p.row_warps * p.rows;
-    for (uint32_t e = threadIdx.x; e < rows * m; e += 256) {
+    for (uint32_t e = threadIdx.x; e < rows * m; e += 32 * kWarps) {
         const uint32_t t = e / rows, f = e % rows, o = blockIdx.x * rows + f;
         if (o >= a.n) continue;
         float y = 0.0f;
@@ -319,7 +327,7 @@ int launch_gemv_group(const GemvArgs &p, unsigned grid, cudaStream_t s) {
 template <typename T>
 int launch_gemv_for(const GemvArgs &p, uint32_t nt, uint32_t rg, unsigned grid, cudaStream_t s) {
     if (nt == 1) return rg == 1 ? launch_gemv_group<T, 1, 1>(p, grid, s) : launch_gemv_group<T, 1, 2>(p, grid, s);
-    return rg == 1 ? launch_gemv_group<T, 2, 1>(p, grid, s) : launch_gemv_group<T, 2, 2>(p, grid, s);
+    return rg == 1 ? launch_gemv_group<T, 2, 1>(p, grid, s) : launch_gemv_group<T, 2, 4>(p, grid, s);
 }
 
 }  // namespace
@@ -331,11 +339,20 @@ int int4_gemv(const Int4Args &a, int32_t dtype, int sms, cudaStream_t s) {
     const bool one = a.m == 1;
     const uintptr_t at = reinterpret_cast<uintptr_t>(a.x);
     p.xvec = at % 16 == 0 && (one || a.ldx % 8 == 0) ? 16 : at % 4 == 0 && (one || a.ldx % 2 == 0) ? 4 : 2;
-    // every CTA resident at once (two on each SM) with an equal share of the features, in equal waves where
-    // a share would be more than the CTA's warps hold; few features leave more warps to share the inputs
-    const uint32_t nt = a.m <= 8 ? 1 : 2, slots = uint32_t(sms) * 2, most = 32 * kWarps / 2;
-    const uint32_t waves = (a.n + slots * most - 1) / (slots * most);
-    const uint32_t share = std::max((a.n + slots * waves - 1) / (slots * waves), 16u), rg = share > 16 ? 2 : 1;
+    // Every CTA resident at once with an equal share of the features, in equal waves where a share would be
+    // more than the CTA's warps hold; few features leave more warps to share the inputs.  A warp with more
+    // features reads x less often: 16 where a share holds no more, otherwise 32 (8192 x 28672, one token: 29.7 us;
+    // 16: 33.9; 64: 39.9), or 64 and one CTA on an SM for two token tiles, where x would fill the L1's bandwidth
+    // (16 tokens: 48.6 us; 32: 58.5)
+    const uint32_t nt = a.m <= 8 ? 1 : 2;
+    uint32_t rg = 1, share;
+    for (;;) {
+        const uint32_t slots = uint32_t(sms) * ctas_on_sm(rg), most = 16 * rg * kWarps;
+        const uint32_t waves = (a.n + slots * most - 1) / (slots * most);
+        share = std::max((a.n + slots * waves - 1) / (slots * waves), 16u);
+        if (rg > 1 || share == 16) break;
+        rg = nt == 1 ? 2 : 4;
+    }
     p.row_warps = 1;
     while (p.row_warps * 16 * rg < share) p.row_warps *= 2;
     p.rows = (share + p.row_warps - 1) / p.row_warps;

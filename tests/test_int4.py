@@ -304,6 +304,19 @@ def test_linear(m, n, k, group, dtype):
     assert (buf[:32] == 3).all() and (buf[32 + m * n:] == 3).all()
 
 
+# few tokens against many features (a warp with several tiles of them, several waves of blocks), with rows of
+# scales that can be read as one word and rows that cannot, and x on and off 16 bytes
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("m", [1, 8, 9, 16])
+@pytest.mark.parametrize("n,k,group", [(6001, 392, 32), (6001, 264, 64), (9000, 256, 128), (5100, 387, 32), (7000, 70, 64),
+                                       (80001, 40, 32), (4800, 300, 128), (300, 672, 32)])
+def test_linear_of_few_tokens(m, n, k, group, dtype):
+    q, codes, s, x = case(n, k, group, dtype, m + n + k, m)
+    y = B.int4_linear(x.cuda(), codes.cuda(), s.cuda(), group=group)
+    check(y, *forward_ref(x, q, s, group, None), k + 1, dtype)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("m,n,k,group", SHAPES)
@@ -481,6 +494,19 @@ def test_large_operands_off_16_bytes(m, n, k, group):
     c, a = pack_ref(x)
     ds = B.int4_scale_grad(odd, torch.from_numpy(c).cuda(), torch.from_numpy(a).cuda(), codes.cuda(), k, group=group)
     check(ds, *scale_grad_ref(dy, c, a, q, k, group), m + group, BF)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [2, 11])
+@pytest.mark.parametrize("n,k,at", [(8200, 8191, 0), (4096, 16384, 3)])
+def test_large_weight_of_few_tokens_off_16_bytes(m, n, k, at):
+    q, codes, s, x = case(n, k, 64, BF, m + k, m)
+    flat = torch.zeros(m * k + at, dtype=BF, device="cuda")
+    view = flat[at:].view(m, k)
+    view.copy_(x)
+    y = B.int4_linear(view, codes.cuda(), s.cuda(), group=64)
+    assert torch.equal(flat[at:].view(m, k).cpu(), x)
+    check(y, *forward_ref(x, q, s, 64, None), k + 1, BF)
 
 
 @pytest.mark.gpu
