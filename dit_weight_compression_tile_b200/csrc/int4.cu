@@ -1,6 +1,6 @@
 // The 4-bit group-scaled weight: its quantizer and its reconstruction, and 8-bit activation checkpoints
 // (ep_int4_quantize, ep_int4_dequantize, ep_act8_pack, ep_act8_unpack).  All four read and write each
-// element once: HBM bounds them.
+// element once: HBM's time is the floor.
 #include <algorithm>
 
 #include "int4_gemm.cuh"
@@ -139,8 +139,9 @@ struct PackArgs {
 // subtract, on the pipe that has room.  Tiny a go by quotient_code.  With BF16 activations the quotients are
 // fractions of small numbers, and nine warps in ten have one next to a half: a slow path for all of those
 // took 34 us for 4096 x 8192, comparing and selecting 26 us, rintf and a conversion for each element, on a
-// half-rate pipe, 42 us.  Copying alone takes 16.3 us in this form: the instructions bound it.  CTAs walk over
-// the groups with the next one's loads in flight.
+// half-rate pipe, 42 us.  This form takes 23.2 us (FP16 25.1; copying alone 16.3, the floor 15.6): the
+// instructions bound it (issue slots 79 %, ALU pipe 49 %, FMA pipe 43 % busy).  CTAs walk over the groups with the next one's
+// loads in flight.
 constexpr int kPackBlocks = 5;  // CTAs on an SM (4: the same; 6, with fewer registers: 27.6 us)
 template <typename T>
 __global__ void __launch_bounds__(256, kPackBlocks) act8_pack_kernel(const T *x, int8_t *codes, float *scales, const PackArgs p) {
@@ -201,41 +202,75 @@ __global__ void __launch_bounds__(256, kPackBlocks) act8_pack_kernel(const T *x,
     }
 }
 
-// x = RNE(a c) in the output's type
+// place i of rows of `by`: its row and its place there (a 64-bit division only where i has more bits)
+__device__ __forceinline__ int64_t row_of(int64_t i, uint32_t by, uint32_t &rest) {
+    if (i >> 32) {
+        rest = uint32_t(i % by);
+        return i / by;
+    }
+    rest = uint32_t(i) % by;
+    return uint32_t(i) / by;
+}
+
+// eight elements of a row, `valid` of them, rounded to T; `wide`: every row begins on 16 bytes
+template <typename T>
+__device__ __forceinline__ void store8(T *p, const float (&v)[8], uint32_t valid, bool wide) {
+    if constexpr (sizeof(T) == 4) {
+        if (wide && valid >= 8) {
+            reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+            return;
+        }
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j)
+            if (j < valid) p[j] = v[j];
+    } else {
+        uint16_t h[8];
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) h[j] = Elem<T>::bits(v[j]);
+        if (wide && valid >= 8) {
+            const auto two = [&](int j) { return h[j] | (uint32_t(h[j + 1]) << 16); };
+            *reinterpret_cast<uint4 *>(p) = make_uint4(two(0), two(2), two(4), two(6));
+            return;
+        }
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j)
+            if (j < valid) reinterpret_cast<uint16_t *>(p)[j] = h[j];
+    }
+}
+
+// x = RNE(a c) in the output's type.  A thread for eight features, HBM bounds it (8192 x 8192 to BF16:
+// 51.5 us of a floor of 31; with a store for each element 150 us).
 template <typename T>
 __global__ void __launch_bounds__(256) act8_unpack_kernel(const int8_t *codes, const float *scales, uint32_t k,
-                                                          uint32_t groups, int64_t total, T *out) {
+                                                          uint32_t groups, int64_t total, T *out, bool wide) {
     const uint32_t chunks = (k + 7) / 8;
     const int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
     if (i >= total) return;
-    const int64_t t = i / chunks;
-    const uint32_t k0 = uint32_t(i % chunks) * 8;
+    uint32_t k0;
+    const int64_t t = row_of(i, chunks, k0);
+    k0 *= 8;
     const float a = __ldg(scales + t * groups + k0 / kActGroup);
     const uint2 w = __ldg(reinterpret_cast<const uint2 *>(codes + t * act8_row_bytes(k) + k0));
-    T *dst = out + t * int64_t(k) + k0;
+    float v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float v = a * float(int8_t((j < 4 ? w.x : w.y) >> (8 * (j & 3))));
-        if (k0 + j < k) {
-            if constexpr (sizeof(T) == 4)
-                dst[j] = v;
-            else
-                reinterpret_cast<uint16_t *>(dst)[j] = Elem<T>::bits(v);
-        }
-    }
+    for (int j = 0; j < 8; ++j) v[j] = a * float(int8_t((j < 4 ? w.x : w.y) >> (8 * (j & 3))));
+    store8(out + t * int64_t(k) + k0, v, k - k0, wide);
 }
 
 // Weight: a lane per word of eight inputs, group / 8 neighbouring lanes per group.  Scale s = max / 7
 // rounded to fp32 and then to S (1 where that is 0, NaN with codes 0 where the group has a NaN or an
-// infinity); codes in -7 .. 7.
+// infinity); codes in -7 .. 7.  The exact quotients' instructions bound it (8192 x 8192 BF16, groups of 128:
+// 105 us of a floor of 26): a weight is quantized once.
 template <typename T, typename S>
 __global__ void __launch_bounds__(256) int4_quantize_kernel(const T *w, int64_t ldw, uint32_t k, uint32_t group,
                                                             uint32_t row_lanes, int64_t total, uint32_t *codes,
                                                             S *scales, bool aligned) {
     const int64_t id = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;  // row_lanes (a multiple of 16) per row
     const bool in = id < total;
-    const int64_t o = in ? id / row_lanes : 0;
-    const uint32_t j = uint32_t(in ? id % row_lanes : 0), k0 = 8 * j;
+    uint32_t j;
+    const int64_t o = row_of(in ? id : 0, row_lanes, j);
+    const uint32_t k0 = 8 * j;
     float v[8];
     load8<T>(w + o * ldw + k0, in ? int64_t(k) - k0 : 0, aligned, v);
     const uint32_t lanes = group / 8, top = group_top(v, int(lanes));
@@ -257,21 +292,22 @@ __global__ void __launch_bounds__(256) int4_quantize_kernel(const T *w, int64_t 
         reinterpret_cast<uint16_t *>(scales)[o * groups + j / lanes] = bad ? uint16_t(0x7fffu) : Elem<S>::bits(s);
 }
 
-// W = RNE(s q)
+// W = RNE(s q): a thread for a word of eight inputs, HBM bounds it (8192 x 8192: 49.6 us of a floor of 26;
+// with a store for each element 139 us)
 template <typename S>
 __global__ void __launch_bounds__(256) int4_dequantize_kernel(const uint32_t *codes, const S *scales, uint32_t k,
-                                                              uint32_t group, int64_t total, S *out) {
+                                                              uint32_t group, int64_t total, S *out, bool wide) {
     const uint32_t used = (k + 7) / 8, words = uint32_t(int4_row_bytes(k) / 4), groups = (k + group - 1) / group;
     const int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
     if (i >= total) return;
-    const int64_t o = i / used;
-    const uint32_t j = uint32_t(i % used);
+    uint32_t j;
+    const int64_t o = row_of(i, used, j);
     const uint32_t w = __ldg(codes + o * words + j);
     const float s = Elem<S>::f(__ldg(reinterpret_cast<const uint16_t *>(scales) + o * groups + 8 * j / group));
-    uint16_t *dst = reinterpret_cast<uint16_t *>(out) + o * int64_t(k) + 8 * j;
+    float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (8 * j + e < k) dst[e] = Elem<S>::bits(s * float(int((w >> (4 * (e / 2) + 16 * (e & 1))) & 15u) - 8));
+    for (int e = 0; e < 8; ++e) v[e] = s * float(int((w >> (4 * (e / 2) + 16 * (e & 1))) & 15u) - 8);
+    store8(out + o * int64_t(k) + 8 * j, v, k - 8 * j, wide);
 }
 
 bool is16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -336,12 +372,13 @@ extern "C" int ep_act8_unpack(const void *d_codes, const float *d_scales, int64_
     if (!blocks_of(total, &grid)) return EP_ERR_UNSUPPORTED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const auto *c = static_cast<const int8_t *>(d_codes);
+    const bool wide = is16(d_out) && k * elt % 16 == 0;
     if (dtype == EP_BF16)
-        act8_unpack_kernel<<<grid, 256, 0, s>>>(c, d_scales, uint32_t(k), groups, total, static_cast<__nv_bfloat16 *>(d_out));
+        act8_unpack_kernel<<<grid, 256, 0, s>>>(c, d_scales, uint32_t(k), groups, total, static_cast<__nv_bfloat16 *>(d_out), wide);
     else if (dtype == EP_FP16)
-        act8_unpack_kernel<<<grid, 256, 0, s>>>(c, d_scales, uint32_t(k), groups, total, static_cast<__half *>(d_out));
+        act8_unpack_kernel<<<grid, 256, 0, s>>>(c, d_scales, uint32_t(k), groups, total, static_cast<__half *>(d_out), wide);
     else
-        act8_unpack_kernel<<<grid, 256, 0, s>>>(c, d_scales, uint32_t(k), groups, total, static_cast<float *>(d_out));
+        act8_unpack_kernel<<<grid, 256, 0, s>>>(c, d_scales, uint32_t(k), groups, total, static_cast<float *>(d_out), wide);
     return cudaGetLastError() == cudaSuccess ? EP_OK : EP_ERR_CUDA;
 }
 
@@ -402,11 +439,12 @@ extern "C" int ep_int4_dequantize(const void *d_codes, const void *d_scales, int
     if (!blocks_of(total, &grid)) return EP_ERR_UNSUPPORTED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const auto *c = static_cast<const uint32_t *>(d_codes);
+    const bool wide = is16(d_out) && k % 8 == 0;
     if (dtype == EP_BF16)
         int4_dequantize_kernel<<<grid, 256, 0, s>>>(c, static_cast<const __nv_bfloat16 *>(d_scales), uint32_t(k),
-                                                    uint32_t(group), total, static_cast<__nv_bfloat16 *>(d_out));
+                                                    uint32_t(group), total, static_cast<__nv_bfloat16 *>(d_out), wide);
     else
         int4_dequantize_kernel<<<grid, 256, 0, s>>>(c, static_cast<const __half *>(d_scales), uint32_t(k),
-                                                    uint32_t(group), total, static_cast<__half *>(d_out));
+                                                    uint32_t(group), total, static_cast<__half *>(d_out), wide);
     return cudaGetLastError() == cudaSuccess ? EP_OK : EP_ERR_CUDA;
 }
