@@ -3,7 +3,7 @@
 // Measured on a B200: 8192 x 28672, groups of 128, one token 29.7 us, 8 tokens 33.7, 16 tokens 48.6; groups
 // of 64 and 32, one token 35.0 and 38.3.  The stream alone takes 18.5 us at the copy rate and 20.8 us by these
 // loads: turning codes into operands (9 instructions for 8 weights) and x's passage through L1 are what is left
-// (issue slots 47 %, ALU pipe 53 %, L1 64 % busy).  1024 x 1024: 2.4 us, a launch.
+// (issue slots 55 %, ALU pipe 53 %, L1 64 % busy).  1024 x 1024: 2.4 us, a launch.
 #include <algorithm>
 
 #include "int4_gemm.cuh"

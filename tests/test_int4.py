@@ -310,7 +310,8 @@ def test_linear(m, n, k, group, dtype):
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("m", [1, 8, 9, 16])
 @pytest.mark.parametrize("n,k,group", [(6001, 392, 32), (6001, 264, 64), (9000, 256, 128), (5100, 387, 32), (7000, 70, 64),
-                                       (80001, 40, 32), (4800, 300, 128), (300, 672, 32)])
+                                       (80001, 40, 32), (4800, 300, 128), (300, 672, 32), (1000, 300, 128), (1000, 257, 128),
+                                       (1000, 384, 128), (1000, 384, 64)])
 def test_linear_of_few_tokens(m, n, k, group, dtype):
     q, codes, s, x = case(n, k, group, dtype, m + n + k, m)
     y = B.int4_linear(x.cuda(), codes.cuda(), s.cuda(), group=group)
