@@ -13,7 +13,7 @@ namespace {
 
 enum Product { kForward, kInputGrad, kScaleGrad };
 
-// Tiles of D = a sum over a contraction in steps of 64:
+// Tiles of D = a sum over a contraction in steps of 64 (or 128, see the launch):
 //   forward         D[o, t]: 128 output features x bn tokens, contraction over the inputs k
 //   input gradient  D[k, t]: 128 inputs x bn tokens, contraction over the output features o
 //   scale gradient  D[o, k]: 128 output features x 128 inputs, contraction over the tokens t
@@ -25,9 +25,9 @@ enum Product { kForward, kInputGrad, kScaleGrad };
 // single form (2048 x 8192 x 8192 BF16, forward, input gradient and scale gradient: single 211, 232 and 339 us,
 // paired 184, 189 and 204 us, 1494 to 1351 TFLOP/s of a floor of 169 us; the tensor pipe is then 90 % (scale
 // gradient 75 %) busy, the issue slots 50 to 63 % with the expansion, and the card near its power limit).
-// 17 to 64 tokens: 8192 x 28672 takes 63 to 65 us where the codes' stream takes 18.5: the expansion's and
-// its handshakes' instructions, 320 a step on each scheduler, fill 73 % of the issue slots of the SMs in use;
-// six groups of expansion warps instead of four, more stages and more raw slots changed nothing.
+// 17 to 64 tokens: 8192 x 28672 takes 57 to 65 us where the codes' stream takes 18.5: the expansion's and
+// its handshakes' instructions (in steps of 64, 320 on each scheduler) fill 73 % of the issue slots of the
+// SMs in use; six groups of expansion warps instead of four, more stages and more raw slots changed nothing.
 // Roles: warps 0..15 expand the quantized operand (weight codes, or checkpoint codes in the scale gradient),
 // warps 16..19 turn finished accumulators into output, warp 20 issues the matrix instructions (PAIR: the
 // first CTA's, for both), warp 21 copies the quantized operand's bytes, warp 22 the dense operand (x or
@@ -35,14 +35,15 @@ enum Product { kForward, kInputGrad, kScaleGrad };
 // Rings in shared memory, running on over the tiles:
 //   raw    the quantized operand's bytes, by TMA, slots of four steps, one for each group of four expansion
 //          warps (passing a slot costs a group 400 cycles, a seventh of its work on a step)
-//   stage  one step's operands: 16 KB expanded (16-bit), and the dense tile (up to 256 or, scale gradient,
+//   stage  one step's operands (W 64s of the contraction): 16 KB expanded (16-bit), and the dense tile (up to 256 or, scale gradient,
 //          twice 64 rows of 128 bytes), both rows of 64 elements with the 128-byte swizzle
 // The expanded operand's rows follow the stored codes (64 consecutive inputs of one output feature or
 // token), so the forward's W is K-major (rows o, 64 k), and the input gradient's W^T and the scale
 // gradient's x are MN-major (rows o or t, twice 64 k); dy is MN-major in the scale gradient (rows t, twice
 // 64 o).  Two accumulators in tensor memory: one tile's is read out while the next one's is built.
 // Few tiles: the contraction is split over a cluster's CTAs, whose accumulators (scale gradient: group
-// sums) are joined through distributed shared memory, in rank order.
+// sums) are joined through distributed shared memory, in rank order; over no more CTAs than leave room for all
+// clusters at once (32 tokens, 2048 x 8192, 16 tiles: split over 6 13.0 us, over 8, in two waves, 21.5).
 constexpr uint32_t kGroups = 4, kExpandWarps = 4 * kGroups, kOutWarp0 = kExpandWarps, kOutWarps = 4;
 constexpr uint32_t kMmaWarp = kOutWarp0 + kOutWarps, kRawWarp = kMmaWarp + 1, kDenseWarp0 = kRawWarp + 1, kLoadWarps = 4;
 constexpr uint32_t kQuantBytes = 16384, kBarBytes = 512, kMaxStages = 8, kMaxRaws = 8;
@@ -193,10 +194,13 @@ struct Ring {
     }
 };
 
-template <typename T, int P, bool TMA, bool PAIR>
+// W: 64s of the contraction in a step
+template <typename T, int P, bool TMA, bool PAIR, uint32_t W>
 __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1)
     int4_mma_kernel(const __grid_constant__ MmaArgs p) {
     static_assert(TMA || !PAIR, "a pair copies its dense operand by TMA");
+    static_assert(W == 1 || (W == 2 && TMA && !PAIR && P == kForward), "wide steps");
+    constexpr uint32_t kSpan = 64 * W, kSteps = kSlotSteps / W;  // a step's contraction, steps of a raw slot
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr uint32_t kRawBytes = Shape<P>::kRawBytes, kWide = PAIR ? 256 : 128;
     const Int4Args &a = p.a;
@@ -204,7 +208,7 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
     // registers, which the matrix instructions take their operands from)
     const uint32_t lane = threadIdx.x & 31u, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-    const uint32_t stage_bytes = kQuantBytes + p.dense_bytes;
+    const uint32_t stage_bytes = W * (kQuantBytes + p.dense_bytes);
     const uint32_t raw0 = base + p.stages * stage_bytes, bars = raw0 + p.raws * kRawBytes;
     auto full = [&](uint32_t i) { return bars + 8 * i; };  // both operands of a stage
     auto stage_free = [&](uint32_t i) { return bars + 64 + 8 * i; };
@@ -219,7 +223,7 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
     // this CTA's share of the contraction (whole raw slots)
     const uint32_t splits = PAIR ? 1 : gridDim.y, rank = PAIR ? 0 : blockIdx.y;
     const uint32_t slot_lo = uint32_t(uint64_t(rank) * p.slots / splits), slot_hi = uint32_t(uint64_t(rank + 1) * p.slots / splits);
-    const uint32_t step_lo = slot_lo * kSlotSteps, steps = min(slot_hi * kSlotSteps, p.steps) - step_lo;
+    const uint32_t step_lo = slot_lo * kSteps, steps = min(slot_hi * kSteps, p.steps) - step_lo;
     // a tile's first index of D's rows (this CTA's 128 of them) and of its columns
     auto row0 = [&](uint32_t tile) { return kWide * (tile / p.tiles_b) + 128 * half; };
     auto col0 = [&](uint32_t tile) { return int64_t(tile % p.tiles_b) * p.bn; };
@@ -269,7 +273,7 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
         // gradient) output feature or token r % 64, inputs 64 (r / 64) .. of the tile's 128
         const uint32_t group = warp >> 2, r = 32 * (warp & 3u) + lane, cc = r >> 6;
         const uint32_t group_bits = 31 - __clz(a.group);
-        uint32_t scale[2];
+        uint32_t scale[W][2];
         // the thread's scales in a step (0 where there is none), read one step ahead.  What only a new tile
         // changes is kept: recomputed each step, its division and products cost as much as the expansion
         const uint16_t *scale_row = nullptr;  // of the tile: row r's (forward), or its first row's, at its first k
@@ -280,7 +284,7 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
             if (tile >= p.tiles) return;
             const uint32_t a0 = quant0(tile);
             if constexpr (P == kScaleGrad) {
-                act_row = a.act_scales + int64_t(64 * step_lo + (r & 63u)) * a.act_groups + a0 / 128;
+                act_row = a.act_scales + int64_t(kSpan * step_lo + (r & 63u)) * a.act_groups + a0 / 128;
                 scale_in = a0 < a.k;
             } else if constexpr (P == kForward) {
                 scale_in = a0 + r < a.n;
@@ -288,21 +292,26 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
             } else {
                 scale_k = a0 + 64 * cc;
                 scale_in = scale_k < a.k;
-                scale_row = a.scales + int64_t(64 * step_lo + (r & 63u)) * a.groups + (scale_k >> group_bits);
+                scale_row = a.scales + int64_t(kSpan * step_lo + (r & 63u)) * a.groups + (scale_k >> group_bits);
             }
         };
         auto load_scales = [&](uint32_t i) {  // step i of the tile entered last
-            scale[0] = scale[1] = 0u;
-            if constexpr (P == kScaleGrad) {
-                if (scale_in && 64 * (step_lo + i) + (r & 63u) < a.m) scale[0] = ldg_now32(act_row + int64_t(64 * i) * a.act_groups);
-            } else {
-                const uint32_t k = P == kForward ? 64 * (step_lo + i) : scale_k;
-                const uint16_t *at = P == kForward ? scale_row + (k >> group_bits) : scale_row + int64_t(64 * i) * a.groups;
-                if (scale_in && (P == kForward || 64 * (step_lo + i) + (r & 63u) < a.n)) {
-                    scale[0] = ldg_now16(at);
-                    // one load for groups of 64 and more: every lane's is a line of its own.  Inputs beyond the last
-                    // have codes of 0, which stand for -8: they get the scale 0, which no scale's range can spoil
-                    if (k + 32 < a.k) scale[1] = a.group == 32 ? ldg_now16(at + 1) : scale[0];
+#pragma unroll
+            for (uint32_t w = 0; w < W; ++w) {
+                const uint32_t from = kSpan * i + 64 * w, at_k = kSpan * step_lo + from;  // along the contraction
+                scale[w][0] = scale[w][1] = 0u;
+                if constexpr (P == kScaleGrad) {
+                    if (scale_in && at_k + (r & 63u) < a.m) scale[w][0] = ldg_now32(act_row + int64_t(from) * a.act_groups);
+                } else {
+                    const uint32_t k = P == kForward ? at_k : scale_k;
+                    const uint16_t *at = P == kForward ? scale_row + (k >> group_bits) : scale_row + int64_t(from) * a.groups;
+                    if (scale_in && (P == kForward ? W == 1 || k < a.k : at_k + (r & 63u) < a.n)) {
+                        scale[w][0] = ldg_now16(at);
+                        // one load for groups of 64 and more: every lane's is a line of its own.  Inputs beyond the
+                        // last have codes of 0, which stand for -8: they get the scale 0, which no scale's range can
+                        // spoil
+                        if (k + 32 < a.k) scale[w][1] = a.group == 32 ? ldg_now16(at + 1) : scale[w][0];
+                    }
                 }
             }
         };
@@ -319,7 +328,7 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
                 err = EP_DEC_TIMEOUT;
                 break;
             }
-            const uint32_t left = min(kSlotSteps, steps - at.i), js = mine.i - at.i;
+            const uint32_t left = min(kSteps, steps - at.i), js = mine.i - at.i;
             const bool has = mine.tile == at.tile && js < left;
             at.i += left;
             if (at.i == steps) at.i = 0, at.tile += walkers;
@@ -328,55 +337,62 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
                 if (lane == 0) mbar_arrive(raw_free(raw.at));
                 continue;
             }
-            const uint32_t now[2] = {scale[0], scale[1]};
+            uint32_t now[W][2];
+#pragma unroll
+            for (uint32_t w = 0; w < W; ++w) now[w][0] = scale[w][0], now[w][1] = scale[w][1];
             const uint32_t tile = mine.tile;
             mine.advance(kGroups, steps, walkers);
             if (mine.tile != tile) enter_tile(mine.tile);
             if (mine.tile < p.tiles) load_scales(mine.i);
             const uint32_t src = raw0 + raw.at * kRawBytes;
-            uint32_t out[8][4];
-            if constexpr (P == kScaleGrad) {
-                const float s = __uint_as_float(now[0]) * Act<T>::kScale;
-                uint32_t hi = Elem<T>::bits(s), lo = Elem<T>::bits(s - Elem<T>::f(uint16_t(hi)));
-                hi |= hi << 16;
-                lo |= lo << 16;
-                const uint32_t row = 64 * js + (r & 63u);
 #pragma unroll
-                for (uint32_t i = 0; i < 4; ++i) {
-                    uint32_t q[4];
-                    lds128(q, src + 128 * row + 16 * ((4 * cc + i) ^ (row & 7u)));
+            for (uint32_t w = 0; w < W; ++w) {
+                const uint32_t sub = js * W + w;  // which 64 of the slot's
+                uint32_t out[8][4];
+                if constexpr (P == kScaleGrad) {
+                    const float s = __uint_as_float(now[w][0]) * Act<T>::kScale;
+                    uint32_t hi = Elem<T>::bits(s), lo = Elem<T>::bits(s - Elem<T>::f(uint16_t(hi)));
+                    hi |= hi << 16;
+                    lo |= lo << 16;
+                    const uint32_t row = 64 * sub + (r & 63u);
 #pragma unroll
-                    for (uint32_t e = 0; e < 8; ++e) {
-                        const uint32_t v = Act<T>::pair(q[e / 2], e & 1u);
-                        out[2 * i + e / 4][e & 3u] = Codes<T>::fma2(v, hi, mul2<T>(v, lo));
+                    for (uint32_t i = 0; i < 4; ++i) {
+                        uint32_t q[4];
+                        lds128(q, src + 128 * row + 16 * ((4 * cc + i) ^ (row & 7u)));
+#pragma unroll
+                        for (uint32_t e = 0; e < 8; ++e) {
+                            const uint32_t v = Act<T>::pair(q[e / 2], e & 1u);
+                            out[2 * i + e / 4][e & 3u] = Codes<T>::fma2(v, hi, mul2<T>(v, lo));
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (uint32_t i = 0; i < 2; ++i) {
+                        uint32_t q[4];
+                        if constexpr (P == kForward) {
+                            lds128(q, src + 128 * r + 16 * ((2 * sub + i) ^ (r & 7u)));
+                        } else {
+                            const uint32_t row = 64 * sub + (r & 63u);
+                            lds128(q, src + 64 * row + 16 * ((2 * cc + i) ^ ((row >> 1) & 3u)));
+                        }
+                        const uint32_t s2 = now[w][i] | (now[w][i] << 16);
+#pragma unroll
+                        for (uint32_t e = 0; e < 4; ++e) {
+                            code_pairs<T>(q[e], out[4 * i + e]);
+#pragma unroll
+                            for (uint32_t h = 0; h < 4; ++h) out[4 * i + e][h] = mul2<T>(out[4 * i + e][h], s2);
+                        }
                     }
                 }
-            } else {
-#pragma unroll
-                for (uint32_t i = 0; i < 2; ++i) {
-                    uint32_t q[4];
-                    if constexpr (P == kForward) {
-                        lds128(q, src + 128 * r + 16 * ((2 * js + i) ^ (r & 7u)));
-                    } else {
-                        const uint32_t row = 64 * js + (r & 63u);
-                        lds128(q, src + 64 * row + 16 * ((2 * cc + i) ^ ((row >> 1) & 3u)));
-                    }
-                    const uint32_t s2 = now[i] | (now[i] << 16);
-#pragma unroll
-                    for (uint32_t e = 0; e < 4; ++e) {
-                        code_pairs<T>(q[e], out[4 * i + e]);
-#pragma unroll
-                        for (uint32_t h = 0; h < 4; ++h) out[4 * i + e][h] = mul2<T>(out[4 * i + e][h], s2);
-                    }
+                if (w == 0 && !mbar_wait(stage_free(stage.at), stage.phase ^ 1u)) {
+                    err = EP_DEC_TIMEOUT;
+                    break;
                 }
-            }
-            if (!mbar_wait(stage_free(stage.at), stage.phase ^ 1u)) {
-                err = EP_DEC_TIMEOUT;
-                break;
-            }
-            const uint32_t dst = base + stage.at * stage_bytes + 128 * r;
+                const uint32_t dst = base + stage.at * stage_bytes + w * kQuantBytes + 128 * r;
 #pragma unroll
-            for (uint32_t i = 0; i < 8; ++i) sts128(dst + 16 * (i ^ (r & 7u)), out[i]);
+                for (uint32_t i = 0; i < 8; ++i) sts128(dst + 16 * (i ^ (r & 7u)), out[i]);
+            }
+            if (err) break;
             // the stores are visible to the matrix unit, and the loads that fed them are done, so that the slot can
             // be written again (freed before the stores, loads still under way returned the next slot's bytes)
             fence_proxy_async();
@@ -479,8 +495,7 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t d = tmem + acc.at * p.bn;
             for (uint32_t i = 0; i < steps; ++i) {
-                const uint32_t quant = base + stage.at * stage_bytes, dense = quant + kQuantBytes;
-                const uint64_t dq = desc128(quant, P == kForward ? 0 : 8192), dd = desc128(dense, P == kScaleGrad ? 8192 : 0);
+                const uint32_t quant = base + stage.at * stage_bytes, dense = quant + W * kQuantBytes;
                 // a step of 16: 32 bytes along K-major rows, 16 rows of 128 bytes of the others
                 constexpr uint64_t kQ = P == kForward ? 2 : 128, kD = P == kScaleGrad ? 128 : 2;
                 if (!mbar_wait(full(stage.at), stage.phase)) {
@@ -491,9 +506,14 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
                 if (half == 0) {
                     if (elected) {
 #pragma unroll
-                        for (uint32_t h = 0; h < 4; ++h)
-                            mma_f16<PAIR>(d, P == kScaleGrad ? dd + h * kD : dq + h * kQ, P == kScaleGrad ? dq + h * kQ : dd + h * kD,
-                                          p.idesc, i > 0 || h > 0);
+                        for (uint32_t w = 0; w < W; ++w) {
+                            const uint64_t dq = desc128(quant + w * kQuantBytes, P == kForward ? 0 : 8192);
+                            const uint64_t dd = desc128(dense + w * p.dense_bytes, P == kScaleGrad ? 8192 : 0);
+#pragma unroll
+                            for (uint32_t h = 0; h < 4; ++h)
+                                mma_f16<PAIR>(d, P == kScaleGrad ? dd + h * kD : dq + h * kQ,
+                                              P == kScaleGrad ? dq + h * kQ : dd + h * kD, p.idesc, i > 0 || w > 0 || h > 0);
+                        }
                         mma_commit<PAIR>(stage_free(stage.at));
                     }
                 } else if (elected) {
@@ -544,14 +564,18 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
                         err = EP_DEC_TIMEOUT;
                         break;
                     }
-                    const uint32_t dst = base + stage.at * stage_bytes + kQuantBytes, bar = full(stage.at);
-                    const uint32_t c = 64 * (step_lo + i);
-                    mbar_expect(bar, p.dense_bytes);
-                    if constexpr (P == kScaleGrad) {
-                        tma_load(dst, &p.dense, b0, c, bar);
-                        tma_load(dst + 8192, &p.dense, b0 + 64, c, bar);
-                    } else {
-                        tma_load(dst, &p.dense, c, b0, bar);
+                    const uint32_t bar = full(stage.at);
+                    mbar_expect(bar, W * p.dense_bytes);
+#pragma unroll
+                    for (uint32_t w = 0; w < W; ++w) {
+                        const uint32_t dst = base + stage.at * stage_bytes + W * kQuantBytes + w * p.dense_bytes;
+                        const uint32_t c = kSpan * (step_lo + i) + 64 * w;  // (beyond the contraction: zeros)
+                        if constexpr (P == kScaleGrad) {
+                            tma_load(dst, &p.dense, b0, c, bar);
+                            tma_load(dst + 8192, &p.dense, b0 + 64, c, bar);
+                        } else {
+                            tma_load(dst, &p.dense, c, b0, bar);
+                        }
                     }
                 }
             }
@@ -670,14 +694,43 @@ Int4Args args_of(int64_t n, int64_t k, int32_t group, const void *codes, const v
 }
 constexpr size_t kSmemMost = 232448;
 
+// How many clusters of `size` CTAs, one on each SM, run at once on the current device: a cluster lies within one
+// GPC, whose SMs it may not use up (looked up once per device and size)
+uint32_t clusters_at_once(int device, uint32_t size) {
+    static std::atomic<int> known[64][9];
+    int n = known[device][size].load();
+    if (n) return uint32_t(n);
+    const auto kern = int4_mma_kernel<__nv_bfloat16, kForward, true, false, 1>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1, size);
+    cfg.blockDim = dim3((kDenseWarp0 + 1) * 32);
+    cfg.dynamicSmemBytes = kSmemMost;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = size;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemMost)) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();  // (a query's error is not the launch's)
+        return 0;
+    }
+    known[device][size].store(n);
+    return uint32_t(n);
+}
+
 // the launch: single or paired CTAs, tiles, the contraction's split, rings as deep as fit
 template <typename T, int P>
 int launch_mma(const Int4Args &a, int sms, cudaStream_t s) {
     MmaArgs p{};
     p.a = a;
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess || device < 0 || device >= 64) return EP_ERR_CUDA;
     const int64_t contraction = P == kForward ? a.k : P == kInputGrad ? int64_t(a.n) : a.m;
-    p.steps = uint32_t((contraction + 63) / 64);
-    p.slots = (p.steps + kSlotSteps - 1) / kSlotSteps;
+    const uint32_t sixty_fours = uint32_t((contraction + 63) / 64);
+    p.slots = (sixty_fours + kSlotSteps - 1) / kSlotSteps;
     const uint64_t dense_cols = P == kForward ? a.k : a.n;
     const int64_t ld = a.m > 1 ? a.ldx : int64_t((dense_cols + 7) / 8 * 8);
     const bool tma = !misaligned(a.x, 16) && ld % 8 == 0 && ld < (int64_t(1) << 38) && a.m <= 0x7fffffff;
@@ -705,9 +758,18 @@ int launch_mma(const Int4Args &a, int sms, cudaStream_t s) {
     p.tiles = uint32_t(tiles_a * tiles_b);
     p.tiles_b = uint32_t(tiles_b);
     uint32_t splits = 1;
-    if (!pair && p.tiles < uint32_t(sms))
+    if (!pair && p.tiles < uint32_t(sms)) {
         splits = std::max(1u, std::min({8u, sms / p.tiles, p.slots}));
-    const uint32_t stage = kQuantBytes + p.dense_bytes, raw = Shape<P>::kRawBytes;
+        while (splits > 1 && p.tiles > clusters_at_once(device, splits)) --splits;
+    }
+    // Steps of 128 spend fewer instructions on their barriers, where they leave three raw slots: forward, 17
+    // tokens, 8192 x 28672 56.7 us against 63.1, 48 tokens 60.5 against 64.2, 4096 x 4096 11.5 against 12.2; with 64
+    // tokens, and two slots, 83.7 against 64.6; the input gradient, one token, 8192 x 8192 29.9 against 24.7
+    constexpr uint32_t kWide = P == kForward ? 2 : 1;
+    const bool wide = kWide == 2 && tma && !pair && p.bn <= 48 && sixty_fours >= 8 * splits;
+    const uint32_t w = wide ? kWide : 1;
+    p.steps = (sixty_fours + w - 1) / w;
+    const uint32_t stage = w * (kQuantBytes + p.dense_bytes), raw = Shape<P>::kRawBytes;
     // 64 KB of raw slots where that leaves five stages, otherwise two slots and as many stages as fit
     // (2048 x 8192 x 8192 forward, paired: 4 slots and 5 stages 187 us, 2 and 6 195 us)
     const uint32_t room = uint32_t(kSmemMost - kBarBytes);
@@ -734,13 +796,12 @@ int launch_mma(const Int4Args &a, int sms, cudaStream_t s) {
     if (tma && !tensor_map(&p.dense, a.x, dt, 2, dense_cols, uint64_t(a.m), uint64_t(ld) * 2, 64,
                            P == kScaleGrad ? 64 : p.dense_bytes / 128))
         return EP_ERR_CUDA;
-    const uint32_t form = pair ? 2 : tma ? 1 : 0;
-    const auto kern = pair  ? int4_mma_kernel<T, P, true, true>
-                      : tma ? int4_mma_kernel<T, P, true, false>
-                            : int4_mma_kernel<T, P, false, false>;
-    static std::atomic<uint64_t> allowed[3];  // devices on which the kernel may use kSmemMost
-    int device = 0;
-    if (cudaGetDevice(&device) != cudaSuccess || device < 0 || device >= 64) return EP_ERR_CUDA;
+    const uint32_t form = pair ? 2 : wide ? 3 : tma ? 1 : 0;
+    const auto kern = pair   ? int4_mma_kernel<T, P, true, true, 1>
+                      : wide ? int4_mma_kernel<T, P, true, false, kWide>
+                      : tma  ? int4_mma_kernel<T, P, true, false, 1>
+                             : int4_mma_kernel<T, P, false, false, 1>;
+    static std::atomic<uint64_t> allowed[4];  // devices on which the kernel may use kSmemMost
     if (!(allowed[form].load() >> device & 1u)) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemMost)) != cudaSuccess)
             return EP_ERR_CUDA;

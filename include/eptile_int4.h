@@ -23,7 +23,7 @@
  * m = 0 does nothing (ep_int4_scale_grad: writes zeros).
  *
  * Every call is asynchronous on `stream`, allocates nothing, needs no workspace, keeps nothing between
- * calls and gives the same bits on every call; calls may overlap and be captured into graphs.
+ * calls and gives the same bits on every call on one GPU; calls may overlap and be captured into graphs.
  * d_status (nullable device uint32): EP_DEC_TIMEOUT is ORed in if a copy into shared memory does not
  * complete within the kernels' poll limit (the output is then not valid).
  * EP_ERR_INVALID_ARG: a null or misaligned pointer, sizes below 1 (m below 0) or above 2^30, another group

@@ -9,6 +9,9 @@ result is rounded once (u, or 2^-25 absolute)."""
 import copy
 import ctypes as C
 import io
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -19,6 +22,7 @@ from dit_weight_compression_tile_b200 import binding as B
 from dit_weight_compression_tile_b200.linear import GroupedINT4Linear, int4_group_linear
 
 BF, HF = torch.bfloat16, torch.float16
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 U = {BF: 2.0 ** -8, HF: 2.0 ** -11}
 SUB = {BF: 2.0 ** -133, HF: 2.0 ** -25}  # half the smallest subnormal
 
@@ -495,6 +499,47 @@ def test_large_operands_off_16_bytes(m, n, k, group):
     c, a = pack_ref(x)
     ds = B.int4_scale_grad(odd, torch.from_numpy(c).cuda(), torch.from_numpy(a).cuda(), codes.cuda(), k, group=group)
     check(ds, *scale_grad_ref(dy, c, a, q, k, group), m + group, BF)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", [(17, 8192, 8192), (48, 4096, 16384), (40, 2048, 8192), (64, 2048, 2048), (100, 1536, 4000)])
+def test_same_bits_of_few_tokens(m, n, k):
+    """the same for contractions split over clusters of several sizes, and steps of 128"""
+    torch.manual_seed(n)
+    codes, s = B.int4_quantize(torch.randn(n, k, device="cuda") * 0.02, 64, dtype=BF)
+    x, dy = torch.randn(m, k, device="cuda").to(BF), torch.randn(m, n, device="cuda").to(BF)
+    act = B.act8_pack(x)
+    wd = B.int4_dequantize(codes, s, k, 64).float()
+    calls = [lambda: B.int4_linear(x, codes, s, group=64), lambda: B.int4_linear_dx(dy, codes, s, k, group=64),
+             lambda: B.int4_scale_grad(dy, *act, codes, k, group=64)]
+    first = [c() for c in calls]
+    for _ in range(20):
+        for f, c in zip(first, calls):
+            assert torch.equal(f, c())
+    for got, a, b, terms in ((first[0], x.float(), wd.T, k), (first[1], dy.float(), wd, n)):  # bounds as above
+        ref, mag = a @ b, a.abs() @ b.abs()
+        tol = (2 * U[BF] + terms * 2.0 ** -22) * mag + U[BF] * ref.abs() + 1e-6
+        assert bool(((got.float() - ref).abs() <= tol).all())
+
+
+@pytest.mark.gpu
+def test_a_first_call_inside_a_capture():
+    """a process whose first product is captured: what the launch asks about the device does not disturb it"""
+    code = """
+import torch
+import dit_weight_compression_tile_b200 as ep
+codes, s = ep.int4_quantize(torch.randn(2048, 2048, device="cuda").bfloat16())
+for m in (5, 33, 600):
+    x = torch.randn(m, 2048, device="cuda").bfloat16()
+    y = torch.empty(m, 2048, device="cuda", dtype=torch.bfloat16)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ep.int4_linear(x, codes, s, out=y)
+    g.replay()
+    assert torch.equal(y, ep.int4_linear(x, codes, s)), m
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=ROOT)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 @pytest.mark.gpu
