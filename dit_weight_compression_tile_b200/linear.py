@@ -23,6 +23,7 @@ import dataclasses
 import torch
 import torch.nn as nn
 import torch.nn.functional as F
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import binding as B
@@ -281,7 +282,12 @@ def int4_group_linear(x, codes, scales, bias=None, group=128):
     backward into a CUDA graph while an eager graph of the same leaves is alive.)"""
     if not torch.is_tensor(x) or x.dim() < 1:
         raise B.EpError(-1, "x must be a (..., in_features) tensor")
-    return _Int4GroupLinear.apply(x, codes, scales, bias, group)
+    if (x.requires_grad or (scales is not None and scales.requires_grad) or (bias is not None and bias.requires_grad)) \
+            and torch.is_grad_enabled() or forward_ad._current_level >= 0:  # (forward mode: refused there)
+        return _Int4GroupLinear.apply(x, codes, scales, bias, group)
+    # nothing to differentiate: no checkpoint, and no autograd function around the call (10 us of the host's time)
+    y, _ = B.int4_layer_forward(x if x.dim() == 2 else x.reshape(-1, x.shape[-1]), codes, scales, group, bias, False)
+    return y if x.dim() == 2 else y.reshape(*x.shape[:-1], y.shape[1])
 
 
 class GroupedINT4Linear(nn.Module):

@@ -748,6 +748,28 @@ def test_layer_keeps_only_what_the_backward_needs():
 
 
 @pytest.mark.gpu
+def test_no_checkpoint_without_a_gradient(monkeypatch):
+    kept = []
+    forward = B.int4_layer_forward
+    monkeypatch.setattr(B, "int4_layer_forward", lambda *a: kept.append(a[5]) or forward(*a))
+    _, codes, s, x = case(40, 130, 64, BF, 3, 6)
+    codes, s, x = codes.cuda(), s.cuda().requires_grad_(True), x.cuda()
+    y = int4_group_linear(x, codes, s, group=64)
+    with torch.no_grad():
+        y0 = int4_group_linear(x.view(2, 3, 130), codes, s, group=64)
+    with torch.inference_mode():
+        y1 = int4_group_linear(x, codes, s, group=64)
+    y2 = int4_group_linear(x.detach(), codes, s.detach(), group=64)
+    assert y.requires_grad and not y0.requires_grad and not y2.requires_grad and y0.shape == (2, 3, 40)
+    assert all(torch.equal(y, t.reshape(6, 40)) for t in (y0, y1, y2))
+    assert kept == [True, False, False, False]
+    with torch.autograd.forward_ad.dual_level():
+        dual = torch.autograd.forward_ad.make_dual(x, torch.ones_like(x))
+        with pytest.raises((RuntimeError, NotImplementedError)):
+            int4_group_linear(dual, codes, s.detach(), group=64)
+
+
+@pytest.mark.gpu
 def test_training_the_scales_runs():
     torch.manual_seed(0)
     layers = nn.Sequential(*[GroupedINT4Linear.from_linear(nn.Linear(a, b, dtype=BF, device="cuda"), group=64,
