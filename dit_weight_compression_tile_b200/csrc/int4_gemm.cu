@@ -432,7 +432,9 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t from = tmem + ((32u * q) << 16) + acc.at * p.bn;
             if constexpr (P == kScaleGrad) {
-                // its row of D times its codes, summed over 32 inputs, then over a group
+                // its row of D times its codes, summed over 32 inputs, then over a group.  The columns behind the last
+                // input are left out: an infinite dy times their zeros is NaN, not a part of the formula
+                const uint32_t inputs = a.k - uint32_t(b0);
                 uint16_t *out = a.out + int64_t(o) * a.groups + b0 / a.group;
                 float sum = 0.0f;
 #pragma unroll
@@ -443,6 +445,11 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
                     for (uint32_t h = 0; h < 2; ++h) {
                         uint32_t d[16];
                         tmem_load16(d, from + 32 * c + 16 * h);
+                        if (32 * c + 16 * h + 16 > inputs) {
+#pragma unroll
+                            for (uint32_t e = 0; e < 16; ++e)
+                                if (32 * c + 16 * h + e >= inputs) d[e] = 0u;
+                        }
 #pragma unroll
                         for (uint32_t e = 0; e < 16; ++e) {
                             // (2^23 + the code, less 2^23 + 8: a conversion runs at an eighth of the rate)
