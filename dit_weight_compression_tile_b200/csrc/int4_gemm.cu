@@ -432,11 +432,9 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t from = tmem + ((32u * q) << 16) + acc.at * p.bn;
             if constexpr (P == kScaleGrad) {
-                // its row of D times its codes, summed over 32 inputs, then over a group.  The columns behind the last
-                // input are left out: an infinite dy times their zeros is NaN, not a part of the formula
-                const uint32_t inputs = a.k - uint32_t(b0);
+                // its row of D times its codes, summed over 32 inputs, then over a group
                 uint16_t *out = a.out + int64_t(o) * a.groups + b0 / a.group;
-                float sum = 0.0f;
+                float sum = 0.0f, all = 0.0f;
 #pragma unroll
                 for (uint32_t c = 0; c < kWide / 32; ++c) {
                     const uint32_t w[4] = {codes[c].x, codes[c].y, codes[c].z, codes[c].w};
@@ -445,11 +443,6 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
                     for (uint32_t h = 0; h < 2; ++h) {
                         uint32_t d[16];
                         tmem_load16(d, from + 32 * c + 16 * h);
-                        if (32 * c + 16 * h + 16 > inputs) {
-#pragma unroll
-                            for (uint32_t e = 0; e < 16; ++e)
-                                if (32 * c + 16 * h + e >= inputs) d[e] = 0u;
-                        }
 #pragma unroll
                         for (uint32_t e = 0; e < 16; ++e) {
                             // (2^23 + the code, less 2^23 + 8: a conversion runs at an eighth of the rate)
@@ -457,6 +450,7 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
                             s = fmaf(__uint_as_float(d[e]), __uint_as_float(0x4b000000u | code) - 8388616.0f, s);
                         }
                     }
+                    all += s;
                     if (splits > 1) {
                         joint[4 * (32 * q + lane) + c] = s;
                         continue;
@@ -466,6 +460,32 @@ __global__ void __launch_bounds__((kDenseWarp0 + (TMA ? 1 : kLoadWarps)) * 32, 1
                         if (o < a.n && b0 / a.group + c * 32 / a.group < a.groups) out[c * 32 / a.group] = Elem<T>::bits(sum);
                         sum = 0.0f;
                     }
+                }
+                // Where a sum is NaN, the group that k ends in again, without the columns behind the last input: an
+                // infinite dy times their zeros is NaN and no part of the formula.  (Left out in the loop above, with
+                // an index compared for every column or every 16, they made 1024 x 4096 x 4096 35.3 us instead of 33.4.)
+                const uint32_t inputs = a.k - uint32_t(b0);
+                if (inputs < kWide && inputs % a.group != 0 && __any_sync(0xffffffffu, all != all)) {
+                    const uint32_t g = inputs / a.group;
+                    sum = 0.0f;
+                    for (uint32_t c = g * a.group / 32; c < (g + 1) * a.group / 32; ++c) {
+                        const uint32_t *w = a.codes + int64_t(min(o, a.n - 1)) * a.words + b0 / 8 + 4 * c;
+                        float s = 0.0f;
+#pragma unroll 1
+                        for (uint32_t h = 0; h < 2; ++h) {
+                            uint32_t d[16];
+                            tmem_load16(d, from + 32 * c + 16 * h);
+#pragma unroll
+                            for (uint32_t e = 0; e < 16; ++e) {
+                                const uint32_t in = e & 7u, at = 32 * c + 16 * h + e;
+                                const uint32_t code = at < inputs ? (__ldg(w + 2 * h + e / 8) >> (4 * (in / 2) + 16 * (in & 1u))) & 15u : 8u;
+                                s = fmaf(at < inputs ? __uint_as_float(d[e]) : 0.0f, float(int(code) - 8), s);
+                            }
+                        }
+                        if (splits > 1) joint[4 * (32 * q + lane) + c] = s;
+                        sum += s;
+                    }
+                    if (splits == 1 && o < a.n) out[g] = Elem<T>::bits(sum);
                 }
             } else {
                 const uint32_t J = P == kForward ? a.n : a.k, f = 32 * q + lane, j = a0 + f;
