@@ -72,6 +72,35 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
+// The sums of the elements of a warp's lanes in `bad` (of `o` and `t`), input by input as the formula has them, in
+// 64 bits: x[t, k] s[o, k / group] q[o, k], each lane every 32nd input, added across the warp in a fixed order.
+// For sums that came out infinite or NaN: an infinite scale times a group's sum hides an input whose product is
+// NaN, or is of the other sign, and sums of x q may pass fp32's range where the scale brings them back (BF16).
+// (Out of line: no call of finite sums pays for it.)
+template <typename T>
+__device__ __noinline__ float formula_sums(const Int4Args *a, uint32_t bad, uint32_t o, uint32_t t, float y) {
+    const uint32_t lane = threadIdx.x & 31u;
+    for (; bad; bad &= bad - 1) {
+        const uint32_t from = __ffs(bad) - 1;
+        const uint32_t row = __shfl_sync(0xffffffffu, o, from), token = __shfl_sync(0xffffffffu, t, from);
+        const uint32_t *codes = a->codes + int64_t(row) * a->words;
+        const uint16_t *scales = a->scales + int64_t(row) * a->groups, *x = a->x + int64_t(token) * a->ldx;
+        double sum = 0.0;
+        for (uint32_t k0 = 0; k0 < a->k; k0 += 32) {
+            const uint32_t k = k0 + lane, e = k & 7u;
+            if (k < a->k) {
+                const int q = int((__ldg(codes + k / 8) >> (4 * (e / 2) + 16 * (e & 1u))) & 15u) - 8;
+                sum += double(Elem<T>::f(__ldg(x + k))) * (double(Elem<T>::f(__ldg(scales + k / a->group))) * double(q));
+            }
+            if (__any_sync(0xffffffffu, sum != sum)) break;  // NaN stays
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (lane == from) y = float(sum);
+    }
+    return y;
+}
+
 struct GemvArgs {
     Int4Args a;
     uint32_t blocks;     // of 128 inputs
@@ -297,12 +326,17 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_on_sm(RG)) int4_gemv_kernel(
     __syncthreads();
     // each feature's slices in order, the bias, one rounding
     const uint32_t rows = p.row_warps * p.rows;
-    for (uint32_t e = threadIdx.x; e < rows * m; e += 32 * kWarps) {
-        const uint32_t t = e / rows, f = e % rows, o = blockIdx.x * rows + f;
-        if (o >= a.n) continue;
+    for (uint32_t e0 = 32 * warp; e0 < rows * m; e0 += 32 * kWarps) {
+        const uint32_t e = e0 + lane, t = e / rows, f = e % rows, o = blockIdx.x * rows + f;
+        const bool mine = e < rows * m && o < a.n;
         float y = 0.0f;
-        for (uint32_t q = 0; q < slices; ++q) y += part[f / p.rows * slices + q][f % p.rows][t];
-        y *= Codes<T>::kUnit;
+        if (mine) {
+            for (uint32_t q = 0; q < slices; ++q) y += part[f / p.rows * slices + q][f % p.rows][t];
+            y *= Codes<T>::kUnit;
+        }
+        const uint32_t bad = __ballot_sync(0xffffffffu, mine && !(fabsf(y) < __uint_as_float(0x7f800000u)));
+        if (bad) y = formula_sums<T>(&p.a, bad, o, t, y);
+        if (!mine) continue;
         if (a.bias) y += Elem<T>::f(__ldg(a.bias + o));
         a.out[int64_t(t) * a.n + o] = Elem<T>::bits(y);
     }

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from dit_weight_compression_tile_b200 import binding as B
-from test_int4 import BF, HF, case, check, pack_ref, scale_grad_ref, store
+from test_int4 import BF, HF, case, check, pack_ref, per_input, scale_grad_ref, store
 
 
 def same_infinities(got, want):
@@ -45,3 +45,53 @@ def test_scale_grad_of_infinite_gradients(m, n, k, group, dtype):
     rows = fine.all(1)
     assert rows.sum() == n - 5
     check(ds[torch.from_numpy(rows)], ref[rows], mag[rows], sub[rows], m + group, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("n,k,group", [(150, 1, 32), (150, 200, 64), (130, 1027, 128), (5100, 330, 32), (40, 72, 64)])
+@pytest.mark.parametrize("m", [1, 2, 9, 16])
+def test_infinite_scales(m, n, k, group, dtype):
+    """an infinite scale spoils its feature as the formula does: inf where all of its products have one sign, NaN
+    where one is 0 or two differ"""
+    q, _, s, x = case(n, k, group, dtype, 4, m)
+    x = x.abs() + 0.25
+    q[:3] = np.where(q[:3] == 0, 1, np.minimum(np.abs(q[:3]), 7))
+    q[3, :] = 2
+    q[3, k - 1] = 0
+    s[0, 0] = s[1, -1] = s[3, -1] = s[10, 0] = float("inf")
+    s[2, 0] = float("-inf")
+    if m > 1:
+        x[1, 0] = 0
+    with np.errstate(invalid="ignore"):
+        w = q * per_input(s, group, k)
+        xd = x.double().numpy()
+        ref = np.stack([(xd * w[o]).sum(1) for o in (0, 1, 2, 3, 10)], 1)
+    assert ref[0, 0] == np.inf and ref[0, 1] == np.inf and ref[0, 2] == -np.inf and np.isnan(ref[0, 3])
+    y = B.int4_linear(x.cuda(), store(q).cuda(), s.cuda(), group=group).cpu()
+    same_infinities(y[:, [0, 1, 2, 3, 10]], ref)
+    rest = [o for o in range(n) if o not in (0, 1, 2, 3, 10)]
+    y0, mag = xd @ w[rest].T, np.abs(xd) @ np.abs(w[rest]).T
+    check(y[:, rest], y0, mag, np.abs(xd).sum(1, keepdims=True), k, dtype)
+    dy = torch.from_numpy(np.random.default_rng(1).normal(size=(m, n))).to(dtype).abs() + 0.25
+    with np.errstate(invalid="ignore"):
+        want = (dy.double().numpy()[:, :, None] * w[None, :, :min(k, 64)]).sum(1) if n < 1000 else None
+    if want is not None:
+        dx = B.int4_linear_dx(dy.cuda(), store(q).cuda(), s.cuda(), k, group=group).cpu()
+        same_infinities(dx[:, :min(k, 64)], want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [1, 5, 8, 9, 16, 17, 40])
+@pytest.mark.parametrize("k,group", [(512, 128), (300, 64), (131, 32)])
+def test_large_activations_under_small_scales(m, k, group):
+    """BF16 activations whose sums of x q pass fp32's range before the scale, and not after it"""
+    n = 70
+    q, codes, s, x = case(n, k, group, BF, 11, m)
+    x = (x.double().clamp(-3, 3) * 1e38).to(BF)
+    bias = torch.ones(n, dtype=BF)
+    y = B.int4_linear(x.cuda(), codes.cuda(), s.cuda(), group=group, bias=bias.cuda())
+    xd, w = x.double().numpy(), q * per_input(s, group, k)
+    ref, mag = xd @ w.T + 1, np.abs(xd) @ np.abs(w).T + 1
+    assert np.abs(ref).max() < 3e38  # the result is in range
+    check(y, ref, mag, np.abs(xd).sum(1, keepdims=True), k + 1, BF)
