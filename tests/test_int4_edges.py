@@ -50,7 +50,7 @@ def test_scale_grad_of_infinite_gradients(m, n, k, group, dtype):
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("n,k,group", [(150, 1, 32), (150, 200, 64), (130, 1027, 128), (5100, 330, 32), (40, 72, 64)])
-@pytest.mark.parametrize("m", [1, 2, 9, 16])
+@pytest.mark.parametrize("m", [1, 2, 9, 16, 17, 40, 300])
 def test_infinite_scales(m, n, k, group, dtype):
     """an infinite scale spoils its feature as the formula does: inf where all of its products have one sign, NaN
     where one is 0 or two differ"""
