@@ -95,3 +95,16 @@ def test_large_activations_under_small_scales(m, k, group):
     ref, mag = xd @ w.T + 1, np.abs(xd) @ np.abs(w).T + 1
     assert np.abs(ref).max() < 3e38  # the result is in range
     check(y, ref, mag, np.abs(xd).sum(1, keepdims=True), k + 1, BF)
+
+
+def test_package_names_follow_their_modules(monkeypatch):
+    """a function replaced in its module is what the package gives from then on, used before or not"""
+    import dit_weight_compression_tile_b200 as ep
+    from dit_weight_compression_tile_b200 import compressed, linear
+    for module, name in ((B, "decompress"), (B, "int4_linear"), (compressed, "TileANSConfig"), (linear, "CompressedLinear")):
+        old = getattr(ep, name)
+        assert old is getattr(module, name)
+        monkeypatch.setattr(module, name, lambda: None)
+        assert getattr(ep, name) is getattr(module, name) is not old
+        monkeypatch.undo()
+        assert getattr(ep, name) is old
