@@ -283,7 +283,9 @@ def int4_group_linear(x, codes, scales, bias=None, group=128):
     if not torch.is_tensor(x) or x.dim() < 1:
         raise B.EpError(-1, "x must be a (..., in_features) tensor")
     if (x.requires_grad or (scales is not None and scales.requires_grad) or (bias is not None and bias.requires_grad)) \
-            and torch.is_grad_enabled() or forward_ad._current_level >= 0:  # (forward mode: refused there)
+            and torch.is_grad_enabled() or forward_ad._current_level >= 0 or torch.jit.is_tracing():
+        # (forward mode: refused there; a trace records the function's call, and of the call below no more than the
+        # allocation of its output)
         return _Int4GroupLinear.apply(x, codes, scales, bias, group)
     # nothing to differentiate: no checkpoint, and no autograd function around the call (10 us of the host's time)
     y, _ = B.int4_layer_forward(x if x.dim() == 2 else x.reshape(-1, x.shape[-1]), codes, scales, group, bias, False)

@@ -1,11 +1,14 @@
 """4-bit group-scaled weights and 8-bit checkpoints at the edges of their formulas.  Formats, references and
 bounds as in test_int4.py."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 from dit_weight_compression_tile_b200 import binding as B
-from test_int4 import BF, HF, case, check, pack_ref, per_input, scale_grad_ref, store
+from dit_weight_compression_tile_b200.linear import GroupedINT4Linear
+from test_int4 import BF, HF, case, check, load, pack_ref, per_input, scale_grad_ref, store
 
 
 def same_infinities(got, want):
@@ -108,3 +111,59 @@ def test_package_names_follow_their_modules(monkeypatch):
         assert getattr(ep, name) is getattr(module, name) is not old
         monkeypatch.undo()
         assert getattr(ep, name) is old
+
+
+def _host_forward(monkeypatch):
+    """the layer's launch replaced by host arithmetic that writes through an address, as a kernel does"""
+    def forward(x, codes, scales, group, bias, checkpoint, *status):
+        w = torch.from_numpy(load(codes, x.shape[1]) * per_input(scales.detach(), group, x.shape[1]))
+        y = x.new_empty((x.shape[0], codes.shape[0]))
+        full = (x.detach().double() @ w.T).to(x.dtype)
+        ctypes.memmove(y.data_ptr(), full.data_ptr(), 2 * int(y.numel()))
+        return y, None
+    monkeypatch.setattr(B, "int4_layer_forward", forward)
+
+
+@pytest.mark.filterwarnings("ignore::DeprecationWarning", "ignore::torch.jit.TracerWarning")
+def test_a_trace_records_the_call(monkeypatch):
+    _host_forward(monkeypatch)
+    q, codes, s, x = case(9, 70, 32, BF, 0, 4)
+    layer = GroupedINT4Linear(70, 9, bias=False, group=32)
+    layer.codes.copy_(codes)
+    layer.scales.data.copy_(s)
+    other = x.flip(0)[:3].contiguous() * 2
+    want, want_other = layer(x), layer(other)
+    for grad in (False, True):  # of a frozen layer, without and with a gradient asked for
+        with torch.set_grad_enabled(grad):
+            traced = torch.jit.trace(layer, (x,), check_trace=False)
+            assert torch.equal(traced(x), want) and torch.equal(traced(other), want_other)
+
+
+@pytest.mark.filterwarnings("ignore::DeprecationWarning", "ignore::torch.jit.TracerWarning")
+def test_calls_without_a_function_refuse_a_trace():
+    q, codes, s, x = case(8, 64, 32, BF, 0, 3)
+    act, a = torch.zeros(3, 64, dtype=torch.int8), torch.ones(3, 1)
+    for call in (lambda t: B.int4_linear(t, codes, s, group=32), lambda t: B.int4_linear_dx(t[:, :8], codes, s, 64, group=32),
+                 lambda t: B.int4_quantize(t, 32)[0], lambda t: B.act8_pack(t)[0],
+                 lambda t: B.int4_scale_grad(t[:, :8], act, a, codes, 64, group=32),
+                 lambda t: B.act8_unpack(act, a, 64) + t, lambda t: B.int4_dequantize(codes, s, 64, 32) + t[:1]):
+        with pytest.raises(B.EpError, match="traced"):
+            torch.jit.trace(call, (x,), check_trace=False)
+
+
+@pytest.mark.gpu
+@pytest.mark.filterwarnings("ignore::DeprecationWarning", "ignore::torch.jit.TracerWarning")
+@pytest.mark.parametrize("train", [False, True])
+@pytest.mark.parametrize("m", [3, 40])
+def test_a_traced_layer_computes(m, train):
+    torch.manual_seed(0)
+    layer = GroupedINT4Linear.from_linear(torch.nn.Linear(256, 96, dtype=BF, device="cuda"), group=64, train_scales=train)
+    x, other = torch.randn(m, 256, device="cuda").to(BF), torch.randn(2, m + 1, 256, device="cuda").to(BF)
+    for grad in (False, True):
+        with torch.set_grad_enabled(grad):
+            traced = torch.jit.trace(layer, (x,), check_trace=False)
+            y = traced(x)
+            assert torch.equal(y, layer(x)) and torch.equal(traced(other), layer(other))
+            if grad and train:
+                ds, want = (torch.autograd.grad(f(x), layer.scales, torch.ones_like(y))[0] for f in (traced, layer))
+                assert torch.equal(ds, want)
