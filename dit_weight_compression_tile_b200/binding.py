@@ -697,15 +697,15 @@ def _launch_scale_grad(dy, ld, act_codes, act_scales, codes, k, group, out, stat
     return out
 
 
-def int4_layer_forward(x, codes, scales, group, bias, checkpoint):
+def int4_layer_forward(x, codes, scales, group, bias, checkpoint, status=None):
     """``int4_linear`` and, with ``checkpoint``, ``act8_pack`` of its input, checked once: (y, act), act one
     int8 tensor with the checkpoint's codes and, from the next multiple of 16 bytes, its scales, or None"""
     n = _int4_linear_check(x, codes, scales, group, bias)
     if _elsewhere(x, None):
         with _made_current(x, None):
-            return int4_layer_forward(x, codes, scales, group, bias, checkpoint)
+            return int4_layer_forward(x, codes, scales, group, bias, checkpoint, status)
     m, k = x.shape
-    y = _launch_linear(x, codes, scales, n, group, bias, x.new_empty((m, n)), None)
+    y = _launch_linear(x, codes, scales, n, group, bias, x.new_empty((m, n)), _status(status, x))
     if not checkpoint:
         return y, None
     size = int(m * ((k + 15) // 16 * 16))  # (a trace's sizes are tensors, and no offsets of an address)
@@ -718,20 +718,21 @@ def int4_layer_forward(x, codes, scales, group, bias, checkpoint):
     return y, act
 
 
-def int4_layer_backward(dy, act, codes, scales, in_features, group, input_grad, scale_grad):
+def int4_layer_backward(dy, act, codes, scales, in_features, group, input_grad, scale_grad, status=None):
     """the gradients (dx, ds) that are asked for (None otherwise) of ``int4_layer_forward``'s y, from what it
     was given and gave: these are not checked again"""
     if _elsewhere(dy, None):
         with _made_current(dy, None):
-            return int4_layer_backward(dy, act, codes, scales, in_features, group, input_grad, scale_grad)
+            return int4_layer_backward(dy, act, codes, scales, in_features, group, input_grad, scale_grad, status)
     dy, ld = _tiles(dy)
     dx = ds = None
+    status = None if status is None else status.data_ptr()
     if input_grad:
-        dx = _launch_dx(dy, ld, codes, scales, in_features, group, dy.new_empty((dy.shape[0], in_features)), None)
+        dx = _launch_dx(dy, ld, codes, scales, in_features, group, dy.new_empty((dy.shape[0], in_features)), status)
     if scale_grad:
         at = act.data_ptr()
         ds = _launch_scale_grad(dy, ld, at, at + dy.shape[0] * ((in_features + 15) // 16 * 16), codes, in_features, group,
-                                dy.new_empty(scales.shape), None)
+                                dy.new_empty(scales.shape), status)
     return dx, ds
 
 

@@ -254,41 +254,45 @@ class _Int4GroupLinear(torch.autograd.Function):
     input, and the input itself can be freed); without it nothing but the weight is kept."""
 
     @staticmethod
-    def forward(ctx, x, codes, scales, bias, group):
+    def forward(ctx, x, codes, scales, bias, group, status):
         x2 = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
-        y, act = B.int4_layer_forward(x2, codes, scales, group, bias, ctx.needs_input_grad[2])
+        y, act = B.int4_layer_forward(x2, codes, scales, group, bias, ctx.needs_input_grad[2], status)
         ctx.save_for_backward(codes, scales, act)
-        ctx.group, ctx.x_shape = group, x.shape
+        ctx.group, ctx.x_shape, ctx.status = group, x.shape, status
         return y if x.dim() == 2 else y.reshape(*x.shape[:-1], codes.shape[0])
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
         codes, scales, act = ctx.saved_tensors
-        need_x, _, need_s, need_b, _ = ctx.needs_input_grad
+        need_x, _, need_s, need_b, _, _ = ctx.needs_input_grad
         dy2 = dy if dy.dim() == 2 else dy.reshape(-1, codes.shape[0])
-        dx, ds = B.int4_layer_backward(dy2, act, codes, scales, ctx.x_shape[-1], ctx.group, need_x, need_s)
+        dx, ds = B.int4_layer_backward(dy2, act, codes, scales, ctx.x_shape[-1], ctx.group, need_x, need_s,
+                                       ctx.status)
         if dx is not None and dy.dim() != 2:
             dx = dx.reshape(ctx.x_shape)
         db = dy2.sum(0, dtype=torch.float32).to(dy.dtype) if need_b else None
-        return dx, None, ds, db, None
+        return dx, None, ds, db, None, None
 
 
-def int4_group_linear(x, codes, scales, bias=None, group=128):
+def int4_group_linear(x, codes, scales, bias=None, group=128, status=None):
     """y = x W^T (+ bias) for x (..., in_features) and a 4-bit group-scaled weight (``int4_quantize``),
     x, scales and bias of one type (BF16 or FP16).  Differentiable in x, scales and bias; the gradient of
     the scales is taken on the input's 8-bit checkpoint (``act8_pack``), about 1/254 of each group of 128
     features' largest magnitude off at most per value.  (As with any such function: do not capture the
-    backward into a CUDA graph while an eager graph of the same leaves is alive.)"""
+    backward into a CUDA graph while an eager graph of the same leaves is alive.)  ``status``: optional int32 tensor on
+    x's device, into which this call and its backward OR EP_DEC_TIMEOUT if a kernel's wait ran out (the results are
+    then not valid)."""
     if not torch.is_tensor(x) or x.dim() < 1:
         raise B.EpError(-1, "x must be a (..., in_features) tensor")
     if (x.requires_grad or (scales is not None and scales.requires_grad) or (bias is not None and bias.requires_grad)) \
             and torch.is_grad_enabled() or forward_ad._current_level >= 0 or torch.jit.is_tracing():
         # (forward mode: refused there; a trace records the function's call, and of the call below no more than the
         # allocation of its output)
-        return _Int4GroupLinear.apply(x, codes, scales, bias, group)
+        return _Int4GroupLinear.apply(x, codes, scales, bias, group, status)
     # nothing to differentiate: no checkpoint, and no autograd function around the call (10 us of the host's time)
-    y, _ = B.int4_layer_forward(x if x.dim() == 2 else x.reshape(-1, x.shape[-1]), codes, scales, group, bias, False)
+    y, _ = B.int4_layer_forward(x if x.dim() == 2 else x.reshape(-1, x.shape[-1]), codes, scales, group, bias, False,
+                                status)
     return y if x.dim() == 2 else y.reshape(*x.shape[:-1], y.shape[1])
 
 
@@ -297,7 +301,9 @@ class GroupedINT4Linear(nn.Module):
     bits per weight.  x is a CUDA tensor of the layer's dtype (BF16 or FP16).  `train_scales` makes the
     scales trainable (the codes stay); the bias is frozen as in the other layers unless its
     requires_grad is set.  A layer built by the constructor holds a zero weight until quantize_weight
-    runs or a checkpoint (codes, scales, bias) is loaded."""
+    runs or a checkpoint (codes, scales, bias) is loaded.  `status` (a buffer of one int32, not part of the
+    checkpoint) stays 0 unless a kernel's wait ran out in a forward or backward since it was last zeroed: it then
+    holds EP_DEC_TIMEOUT (32), and those results are not valid."""
 
     def __init__(self, in_features, out_features, bias=True, *, group=128, train_scales=False, device=None,
                  dtype=torch.bfloat16):
@@ -313,6 +319,7 @@ class GroupedINT4Linear(nn.Module):
                                                  device=device))
         self.scales = nn.Parameter(torch.ones(out_features, -(-in_features // group), dtype=dtype, device=device),
                                    requires_grad=train_scales)
+        self.register_buffer("status", torch.zeros(1, dtype=torch.int32, device=device), persistent=False)
         self.bias = nn.Parameter(torch.zeros(out_features, device=device, dtype=dtype), requires_grad=False) \
             if bias else None
 
@@ -341,6 +348,11 @@ class GroupedINT4Linear(nn.Module):
             self.codes.copy_(codes)
             self.scales.copy_(scales)
 
+    def _load_from_state_dict(self, *args, **kwargs):
+        super()._load_from_state_dict(*args, **kwargs)
+        if "status" in self._buffers:  # not loaded, and without a value after to_empty
+            self.status.zero_()
+
     @property
     def stored_nbytes(self):
         """weight storage: codes and scales, excluding the bias"""
@@ -354,7 +366,8 @@ class GroupedINT4Linear(nn.Module):
         return B.int4_dequantize(self.codes, self.scales.detach(), self.in_features, self.group)
 
     def forward(self, x):
-        return int4_group_linear(x, self.codes, self.scales, self.bias, self.group)
+        # (a layer pickled by an earlier version has no status)
+        return int4_group_linear(x, self.codes, self.scales, self.bias, self.group, self._buffers.get("status"))
 
     def extra_repr(self):
         return (f"in_features={self.in_features}, out_features={self.out_features}, bias={self.bias is not None}, "

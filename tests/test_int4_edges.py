@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from dit_weight_compression_tile_b200 import binding as B
-from dit_weight_compression_tile_b200.linear import GroupedINT4Linear
+from dit_weight_compression_tile_b200.linear import GroupedINT4Linear, int4_group_linear
 from test_int4 import BF, HF, case, check, load, pack_ref, per_input, scale_grad_ref, store
 
 
@@ -167,3 +167,51 @@ def test_a_traced_layer_computes(m, train):
             if grad and train:
                 ds, want = (torch.autograd.grad(f(x), layer.scales, torch.ones_like(y))[0] for f in (traced, layer))
                 assert torch.equal(ds, want)
+
+
+# ---------------------------------------------------------------- waits that run out are reported
+def test_status_is_no_part_of_a_checkpoint():
+    layer = GroupedINT4Linear(70, 9, group=32)
+    assert layer.status.dtype == torch.int32 and layer.status.tolist() == [0]
+    assert set(layer.state_dict()) == {"codes", "scales", "bias"}
+    layer.status.fill_(7)  # as after to_empty
+    layer.load_state_dict(layer.state_dict())
+    assert layer.status.tolist() == [0]
+    del layer._buffers["status"]  # as unpickled from before it had one
+    layer.load_state_dict(layer.state_dict())
+    with pytest.raises(B.EpError):
+        layer(torch.zeros(2, 70, dtype=BF))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [3, 40])
+def test_every_product_of_a_layer_reports_its_waits(m, monkeypatch):
+    """the layer's status word reaches each launch that waits, is left alone by those that end, and keeps its bits"""
+    layer = GroupedINT4Linear.from_linear(torch.nn.Linear(96, 72, dtype=BF, device="cuda"), group=32, train_scales=True)
+    own, given, real = layer.status.data_ptr(), {}, B.lib()
+
+    class Recorder:
+        def __getattr__(self, name):
+            def call(*args):
+                given.setdefault(name, []).append(args[-2])
+                return getattr(real, name)(*args)
+            return call if name in ("ep_int4_linear", "ep_int4_linear_dx", "ep_int4_scale_grad") else getattr(real, name)
+
+    monkeypatch.setattr(B, "lib", Recorder)
+    x = torch.randn(m, 96, device="cuda").to(BF).requires_grad_(True)
+    layer(x).sum().backward()
+    with torch.no_grad():
+        layer(x)
+    assert given == {"ep_int4_linear": [own, own], "ep_int4_linear_dx": [own], "ep_int4_scale_grad": [own]}
+    assert layer.status.tolist() == [0]
+    layer.status.fill_(32)
+    layer(x).sum().backward()
+    assert layer.status.tolist() == [32]
+    given.clear()
+    y = int4_group_linear(x, layer.codes, layer.scales, group=32)
+    torch.autograd.grad(y, (x, layer.scales), torch.ones_like(y))
+    assert given == {"ep_int4_linear": [None], "ep_int4_linear_dx": [None], "ep_int4_scale_grad": [None]}
+    for bad in (torch.zeros(1, dtype=torch.int64, device="cuda"), torch.zeros(1, dtype=torch.int32),
+                torch.zeros(0, dtype=torch.int32, device="cuda")):
+        with pytest.raises(B.EpError):
+            int4_group_linear(x, layer.codes, layer.scales, group=32, status=bad)
