@@ -8,7 +8,7 @@ import torch
 
 from dit_weight_compression_tile_b200 import binding as B
 from dit_weight_compression_tile_b200.linear import GroupedINT4Linear, int4_group_linear
-from test_int4 import BF, HF, case, check, load, pack_ref, per_input, scale_grad_ref, store
+from test_int4 import BF, HF, SHAPES, case, check, load, pack_ref, per_input, scale_grad_ref, store
 
 
 def same_infinities(got, want):
@@ -215,3 +215,129 @@ def test_every_product_of_a_layer_reports_its_waits(m, monkeypatch):
                 torch.zeros(0, dtype=torch.int32, device="cuda")):
         with pytest.raises(B.EpError):
             int4_group_linear(x, layer.codes, layer.scales, group=32, status=bad)
+
+
+# ---------------------------------------------------------------- products of small integers: no tolerance
+# Tokens and gradients of -1, 0, 1 and scales of the type's full length in [1/4, 1/2): every sum below is a multiple
+# of 2^-9 (BF16) or 2^-12 (FP16) and below 2^10 (8192 terms of at most 4, whose random sum has a deviation of 2^7),
+# 22 bits: fp32 holds each one exactly in any order, and the only roundings are the documented ones.  (The checkpoint's
+# scales are powers of two: a c is exact.  Its sums are multiples of 1/2 below 2^15.)
+EXACT = SHAPES + [(2048, 8192, 8192, 128), (17, 8192, 8192, 128), (48, 4096, 4096, 64), (1030, 4090, 4100, 32)]
+
+
+def signs(rows, cols, seed):
+    """-1, 0 or 1, and no zero in the last row and the last column, which a ragged tile would lose first"""
+    v = torch.from_numpy(np.random.default_rng(seed).integers(-1, 2, (rows, cols)))
+    v[-1] = torch.where(v[-1] == 0, 1 - 2 * (torch.arange(cols) % 2), v[-1])
+    v[:, -1] = torch.where(v[:, -1] == 0, -1, v[:, -1])
+    return v.cuda()
+
+
+def exact_weight(n, k, group, dtype, seed):
+    rng = np.random.default_rng(seed)
+    q = rng.integers(-8, 8, (n, k))
+    q[-1, :], q[:, -1] = np.where(q[-1] == 0, 3, q[-1]), np.where(q[:, -1] == 0, -5, q[:, -1])
+    bits = 7 if dtype == BF else 10
+    s = torch.from_numpy(rng.integers(2 ** bits, 2 ** (bits + 1), (n, -(-k // group))) * 2.0 ** -(bits + 2)).to(dtype)
+    w = torch.from_numpy(q).cuda().double() * s.cuda().double().repeat_interleave(group, 1)[:, :k]
+    return store(q).cuda(), s.cuda(), w, torch.from_numpy(q).cuda()
+
+
+def assert_exact(call, want, dtype, mag=None, terms=0, limit=2 ** 11, times=3):
+    """equal to the sum rounded once; a sum that fp32 cannot hold (FP16's multiples of 2^-12 from 2^12 on: 24 bits, one
+    left for the sums on its way) is off by at most 2^-23 of the magnitudes' sum for each term.  (Weights and tokens of
+    one seed, where n = k, agree in sign along the diagonal: 8192 terms of 1.3 on average make 11000 there.)"""
+    exact = want.abs() < limit
+    assert want.abs().max() < 2 ** 15 and exact.float().mean() > 0.99
+    out = want.float().to(dtype)
+    for _ in range(times):
+        got = call()
+        assert got.dtype == dtype and torch.equal(got[exact], out[exact]), int((got != out)[exact].sum())
+        if not exact.all():
+            u, err = torch.finfo(dtype).eps / 2, (got.double() - want).abs()
+            assert (err <= u * want.abs() + (1 + u) * terms * 2.0 ** -23 * mag)[~exact].all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("m,n,k,group", EXACT)
+def test_linear_of_integers(m, n, k, group, dtype):
+    codes, s, w, _ = exact_weight(n, k, group, dtype, m + n)
+    x = signs(m, k, m + k)
+    bias = signs(1, n, n)[0].to(dtype) if n % 2 == 0 else None
+    # up to 16 tokens the weight is exact, above its entries are rounded to the type
+    want, mag = x.double() @ (w if m <= 16 else w.to(dtype).double()).T, x.double().abs() @ w.abs().T
+    want = want if bias is None else want + bias.double()
+    x = x.to(dtype)
+    assert_exact(lambda: B.int4_linear(x, codes, s, group=group, bias=bias), want, dtype, mag + 1, k + 1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("m", [1, 8, 9, 16])
+@pytest.mark.parametrize("n,k,group", [(6001, 392, 32), (9000, 256, 128), (5100, 387, 32), (7000, 70, 64), (300, 672, 32),
+                                       (1000, 257, 128), (1000, 384, 64), (64, 8200, 128)])
+def test_few_tokens_of_integers(m, n, k, group, dtype):
+    codes, s, w, _ = exact_weight(n, k, group, dtype, m + n)
+    x = signs(m, k, m + k)
+    assert_exact(lambda: B.int4_linear(x.to(dtype), codes, s, group=group), x.double() @ w.T, dtype,
+                 x.double().abs() @ w.abs().T, k)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("m,n,k,group", EXACT)
+def test_input_grad_of_integers(m, n, k, group, dtype):
+    codes, s, w, _ = exact_weight(n, k, group, dtype, m + n)
+    dy = signs(m, n, m + n)
+    want, mag = dy.double() @ w.to(dtype).double(), dy.double().abs() @ w.abs()
+    dy = dy.to(dtype)
+    assert_exact(lambda: B.int4_linear_dx(dy, codes, s, k, group=group), want, dtype, mag, n)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("m,n,k,group", EXACT)
+def test_scale_grad_of_integers(m, n, k, group, dtype):
+    codes, _, _, q = exact_weight(n, k, group, dtype, m + n)
+    dy, rng = signs(m, n, m + n), np.random.default_rng(k)
+    c = np.zeros((m, -(-k // 16) * 16), np.int8)
+    c[:, :k] = rng.integers(-3, 4, (m, k))
+    c[-1, :k], c[:, k - 1] = np.where(c[-1, :k] == 0, 2, c[-1, :k]), np.where(c[:, k - 1] == 0, -1, c[:, k - 1])
+    a = torch.from_numpy(2.0 ** rng.integers(-1, 1, (m, -(-k // 128)))).float().cuda()
+    c = torch.from_numpy(c).cuda()
+    p = (dy.double().T @ (c[:, :k].double() * a.double().repeat_interleave(128, 1)[:, :k])) * q
+    want = torch.nn.functional.pad(p, (0, -k % group)).view(n, -1, group).sum(-1)
+    dy = dy.to(dtype)
+    assert_exact(lambda: B.int4_scale_grad(dy, c, a, codes, k, group=group), want, dtype, limit=2 ** 15)
+
+
+@pytest.mark.gpu
+def test_large_fp16_products():
+    """the largest products in FP16 on real-valued inputs, against float64, the weight's rounding included"""
+    m, n, k, group = 2048, 8192, 8192, 128
+    torch.manual_seed(1)
+    codes, s = B.int4_quantize(torch.randn(n, k, device="cuda") * 0.02, group, dtype=HF)
+    x, dy = torch.randn(m, k, device="cuda").to(HF), (torch.randn(m, n, device="cuda") * 0.1).to(HF)
+    w = B.int4_dequantize(codes, torch.ones_like(s), k, group).double() * s.double().repeat_interleave(group, 1)
+    u, sub = 2.0 ** -11, 2.0 ** -25
+    for got, t, v, terms in ((B.int4_linear(x, codes, s, group=group), x.double(), w.T, k),
+                             (B.int4_linear_dx(dy, codes, s, k, group=group), dy.double(), w, n)):
+        ref, mag, rms = t @ v, t.abs() @ v.abs(), (t.square() @ v.square()).sqrt()
+        err, out = (got.double() - ref).abs(), u * ref.abs() * (1 + 2 * u) + sub
+        assert (err <= (u + terms * 2.0 ** -23) * (1 + 2 * u) * mag + out + sub * t.abs().sum(1, keepdim=True)).all()
+        # a weight's rounding is off by at most u |w|, one independent of the next: their sum's deviation is at most
+        # u rms (uniform ones: u rms / sqrt 3), of which 8 are passed with odds below 1e-14 for each of 2^24 results; the
+        # accumulator's steps, 2^-23 of at most 8 rms each, add their number's root
+        assert (err <= 8 * u * rms + 8 * terms ** 0.5 * 2.0 ** -23 * 8 * rms + out).all()
+    act = B.act8_pack(x)
+    ds = B.int4_scale_grad(dy, *act, codes, k, group=group)
+    q = B.int4_dequantize(codes, torch.ones_like(s), k, group).double()
+    c, a = act[0].double(), act[1].double().repeat_interleave(128, 1)
+    fold = lambda p: p.view(n, -1, group).sum(-1)  # noqa: E731
+    ref = fold((dy.double().T @ (c * a)) * q)
+    rms = fold((dy.double().T.square() @ (c * a).square()) * q.square()).sqrt()
+    terms = m + group
+    # as above; a c by u (1 + 2^-1) of itself (its low part's product is rounded too)
+    tol = 8 * 1.5 * u * rms + 8 * terms ** 0.5 * 2.0 ** -23 * 8 * rms + u * ref.abs() * (1 + 2 * u) + sub
+    assert ((ds.double() - ref).abs() <= tol).all()
