@@ -498,12 +498,12 @@ _INT4_DTYPES = (torch.bfloat16, torch.float16)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_tracing = getattr(torch._C, "_is_tracing", None) or torch.jit.is_tracing
 
 
 def _refuse_trace(name):
     """a trace would record the allocation of the output and not the kernel that fills it"""
-    if torch.jit.is_tracing():
-        raise EpError(-1, f"{name} cannot be traced: int4_group_linear and GroupedINT4Linear can")
+    raise EpError(-1, f"{name} cannot be traced: int4_group_linear and GroupedINT4Linear can")
 
 
 def _elsewhere(t, stream):
@@ -592,7 +592,8 @@ def int4_quantize(weight, group=128, dtype=None, stream=None):
     """(codes, scales) of a CUDA BF16 / FP16 / FP32 (out_features, in_features) weight (ep_int4_quantize):
     codes uint8 (out_features, ceil(in_features / 32) * 16), scales (out_features, ceil(in_features /
     group)) of ``dtype`` (torch.bfloat16 or torch.float16; default the weight's, BF16 for FP32)."""
-    _refuse_trace("int4_quantize")
+    if _tracing():
+        _refuse_trace("int4_quantize")
     if weight.dtype not in (torch.bfloat16, torch.float16, torch.float32):
         raise EpError(-8, f"source dtype {weight.dtype}")
     if not weight.is_cuda or weight.dim() != 2 or weight.numel() == 0:
@@ -619,7 +620,8 @@ def int4_quantize(weight, group=128, dtype=None, stream=None):
 
 def int4_dequantize(codes, scales, in_features, group=128, out=None, stream=None):
     """the (out_features, in_features) weight s q in the scales' dtype (ep_int4_dequantize)"""
-    _refuse_trace("int4_dequantize")
+    if _tracing():
+        _refuse_trace("int4_dequantize")
     if scales is None:
         raise EpError(-1, "scales are needed")
     n = _int4_weight(codes, scales, in_features, group)
@@ -740,7 +742,8 @@ def int4_linear(x, codes, scales, group=128, bias=None, out=None, status=None, s
     """Y = X W^T (+ bias) with a 4-bit group-scaled W (ep_int4_linear).  ``x``: CUDA (m, in_features) of the
     scales' dtype, any m, rows any distance apart; ``codes``, ``scales``: from ``int4_quantize``.  Returns
     the contiguous (m, out_features) output."""
-    _refuse_trace("int4_linear")
+    if _tracing():
+        _refuse_trace("int4_linear")
     n = _int4_linear_check(x, codes, scales, group, bias)
     if _elsewhere(x, stream):
         with _made_current(x, stream):
@@ -751,7 +754,8 @@ def int4_linear(x, codes, scales, group=128, bias=None, out=None, status=None, s
 def int4_linear_dx(dy, codes, scales, in_features, group=128, out=None, status=None, stream=None):
     """dX = dY W, the input gradient of ``int4_linear`` (ep_int4_linear_dx).  ``dy``: CUDA (m,
     out_features) of the scales' dtype."""
-    _refuse_trace("int4_linear_dx")
+    if _tracing():
+        _refuse_trace("int4_linear_dx")
     if scales is None:
         raise EpError(-1, "scales are needed")
     n = _int4_weight(codes, scales, in_features, group)
@@ -768,7 +772,8 @@ def int4_linear_dx(dy, codes, scales, in_features, group=128, out=None, status=N
 def act8_pack(x, stream=None):
     """(codes, scales) of an 8-bit checkpoint of CUDA BF16 / FP16 / FP32 (m, features) activations
     (ep_act8_pack): codes int8 (m, ceil(features / 16) * 16), scales fp32 (m, ceil(features / 128))."""
-    _refuse_trace("act8_pack")
+    if _tracing():
+        _refuse_trace("act8_pack")
     if x.dtype not in (torch.bfloat16, torch.float16, torch.float32):
         raise EpError(-8, f"source dtype {x.dtype}")
     if not x.is_cuda or x.dim() != 2 or x.shape[1] < 1:
@@ -792,7 +797,8 @@ def _act8(codes, scales, features):
 
 def act8_unpack(codes, scales, features, dtype=torch.bfloat16, out=None, stream=None):
     """the (m, features) activations a c of a checkpoint, rounded once to ``dtype`` (ep_act8_unpack)"""
-    _refuse_trace("act8_unpack")
+    if _tracing():
+        _refuse_trace("act8_unpack")
     _act8(codes, scales, features)
     if dtype not in (torch.bfloat16, torch.float16, torch.float32):
         raise EpError(-8, f"output dtype {dtype}")
@@ -812,7 +818,8 @@ def int4_scale_grad(dy, act_codes, act_scales, codes, in_features, group=128, ou
     """the gradient of every group scale of ``int4_linear`` (ep_int4_scale_grad): ``dy`` CUDA BF16 / FP16
     (m, out_features), the forward's input as an 8-bit checkpoint (``act8_pack``), the weight's codes.
     Returns (out_features, ceil(in_features / group)) in dy's dtype."""
-    _refuse_trace("int4_scale_grad")
+    if _tracing():
+        _refuse_trace("int4_scale_grad")
     n = _int4_weight(codes, None, in_features, group)
     _act8(act_codes, act_scales, in_features)
     if dy.dtype not in _INT4_DTYPES or dy.dim() != 2 or dy.shape[1] != n:

@@ -286,7 +286,7 @@ def int4_group_linear(x, codes, scales, bias=None, group=128, status=None):
     if not torch.is_tensor(x) or x.dim() < 1:
         raise B.EpError(-1, "x must be a (..., in_features) tensor")
     if (x.requires_grad or (scales is not None and scales.requires_grad) or (bias is not None and bias.requires_grad)) \
-            and torch.is_grad_enabled() or forward_ad._current_level >= 0 or torch.jit.is_tracing():
+            and torch.is_grad_enabled() or forward_ad._current_level >= 0 or B._tracing():
         # (forward mode: refused there; a trace records the function's call, and of the call below no more than the
         # allocation of its output)
         return _Int4GroupLinear.apply(x, codes, scales, bias, group, status)

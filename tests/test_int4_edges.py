@@ -104,13 +104,14 @@ def test_package_names_follow_their_modules(monkeypatch):
     """a function replaced in its module is what the package gives from then on, used before or not"""
     import dit_weight_compression_tile_b200 as ep
     from dit_weight_compression_tile_b200 import compressed, linear
-    for module, name in ((B, "decompress"), (B, "int4_linear"), (compressed, "TileANSConfig"), (linear, "CompressedLinear")):
+    for module, name in ((B, "decompress"), (B, "lib"), (compressed, "TileANSConfig"), (linear, "CompressedLinear")):
         old = getattr(ep, name)
         assert old is getattr(module, name)
         monkeypatch.setattr(module, name, lambda: None)
         assert getattr(ep, name) is getattr(module, name) is not old
         monkeypatch.undo()
         assert getattr(ep, name) is old
+    assert ep.int4_linear is B.int4_linear and ep.int4_group_linear is linear.int4_group_linear
 
 
 def _host_forward(monkeypatch):
