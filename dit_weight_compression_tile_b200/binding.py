@@ -549,7 +549,8 @@ def _tiles(t):
 def _stream_rows(t, weights):
     """``_rows`` for the product that streams the weight: the same where the weight is large (5 tokens: 8192 x
     28671 33.8 us, 72.5 without the copy, at 2^26 weights 16.0 against 24.4; the copy costs the host 5 us, and smaller
-    products are bound by the host's 10)"""
+    products are bound by the host's 10; in a CUDA graph, where they are not, rows on 16 bytes are the caller's to lay
+    out)"""
     t, ld = _rows(t)
     return _aligned_rows(t, ld) if t.shape[0] > 1 and weights >= 1 << 26 else (t, ld)
 

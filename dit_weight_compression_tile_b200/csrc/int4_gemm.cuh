@@ -25,8 +25,9 @@ struct Int4Args {
 int device_sms();
 
 // ep_int4_linear: up to so many tokens (two token tiles) int4_gemv.cu, above it the tcgen05 kernel.  Measured with
-// 16 tokens, the former against the latter: 1024 x 1024 2.7 us against 6.9, 4096 x 4096 6.9 against 11.5,
-// 8192 x 28672 48.6 against 62.9, 8192 x 8192 in groups of 32 22.6 against 26.4; 17 tokens would need a third tile
+// 16 tokens, the former against the latter: 1024 x 1024 2.7 us against 6.6, 4096 x 4096 6.9 against 11.0,
+// 8192 x 28672 48.6 against 82.0, 8192 x 8192 in groups of 32 22.6 against 32.0 (17 tokens, 57 us at 8192 x 28672, would
+// need a third tile)
 constexpr int64_t kGemvTokens = 16;
 int int4_gemv(const Int4Args &a, int32_t dtype, int sms, cudaStream_t s);
 
@@ -89,9 +90,6 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, u
 }
 __device__ __forceinline__ void lds128(uint32_t (&v)[4], uint32_t a) {
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(a));
-}
-__device__ __forceinline__ void lds64(uint32_t *v, uint32_t a) {
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(a));
 }
 
 // all threads of the cluster's CTAs; shared memory written before it is visible to the others after it

@@ -1,9 +1,11 @@
 // ep_int4_linear for few tokens (m <= kGemvTokens): every weight is read once from memory and multiplied
 // for all tokens (0.5 bytes and 2 m flops per weight: HBM's time is the floor).
-// Measured on a B200: 8192 x 28672, groups of 128, one token 29.7 us, 8 tokens 33.7, 16 tokens 48.6; groups
-// of 64 and 32, one token 35.0 and 38.3.  The stream alone takes 18.5 us at the copy rate and 20.8 us by these
-// loads: turning codes into operands (9 instructions for 8 weights) and x's passage through L1 are what is left
-// (issue slots 55 %, ALU pipe 53 %, L1 64 % busy).  1024 x 1024: 2.4 us, a launch.
+// Measured on a B200: 8192 x 28672, groups of 128, one token 29.8 us, 8 tokens 33.8, 16 tokens 47.8; groups
+// of 64 and 32, one token 36.2 and 42.2.  The stream alone takes 18.5 us at the copy rate and 20.8 us by these
+// loads, 25.9 without x's.  No unit is busy enough to bound it (one token: L1 65 %, issue slots 54 %, ALU pipe 53 %, DRAM
+// 45 %): 16 warps on an SM at 122 registers leave it waiting for loads (3.1 cycles an instruction), among which the
+// codes' expansion (9 instructions for 8 weights) and x's reads through L1 come one after the other.  1024 x 1024:
+// 2.4 us, a launch.
 #include <algorithm>
 
 #include "int4_gemm.cuh"

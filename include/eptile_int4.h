@@ -18,8 +18,10 @@
  *
  * Activations and gradients are row-major with rows `ld` elements apart (ld >= the row's length; not
  * read for one row); outputs are contiguous and overlap no input.  Products are summed in fp32 and
- * rounded once to `dtype`; where they run on the tensor cores' 16-bit operands, the weight s q (or the
- * checkpoint's a c) is rounded to `dtype` first.  NaN and infinities propagate as in the formulas.
+ * rounded once to `dtype`.  ep_int4_linear of up to 16 tokens takes q, s and x exactly; above that, and in
+ * ep_int4_linear_dx, the weight s q is rounded to `dtype` first, as is the checkpoint's a c in
+ * ep_int4_scale_grad: an FP16 |s q| from 65520 on (scales from 8192 on) is then infinite, one up to 2^-25
+ * zero.  On what is so rounded, NaN and infinities propagate as in the formulas.
  * m = 0 does nothing (ep_int4_scale_grad: writes zeros).
  *
  * Every call is asynchronous on `stream`, allocates nothing, needs no workspace, keeps nothing between
@@ -72,8 +74,9 @@ int ep_act8_unpack(const void *d_codes, const float *d_scales, int64_t m, int64_
 
 /* The gradient of every group scale from the output's gradient and the forward's checkpointed input:
  * ds[o, g] = sum over k in group g of q[o, k] sum_t dy[t, o] a[t, k / 128] c[t, k], n x ceil(k / group) of
- * dtype.  The weight gradient itself is never written.  dtype EP_FP16 holds a c in 16 bits too: activations
- * beyond its range, which only an FP32 x has, make their groups' sums infinite or NaN. */
+ * dtype.  The weight gradient itself is never written.  dtype EP_FP16 holds a c in FP16 whatever the checkpoint
+ * was made of: of activations that were BF16 or FP32, a group with one from about 65504 on makes its sums
+ * infinite or NaN, and values up to 2^-25 add nothing (up to 2^-14 they lose digits). */
 int ep_int4_scale_grad(const void *d_dy, int64_t lddy, const void *d_act, const float *d_act_scales, int64_t m,
                        const void *d_codes, int64_t n, int64_t k, int32_t group, int32_t dtype, void *d_ds,
                        uint32_t *d_status, ep_stream_t stream);

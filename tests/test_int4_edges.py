@@ -342,3 +342,43 @@ def test_large_fp16_products():
     # as above; a c by u (1 + 2^-1) of itself (its low part's product is rounded too)
     tol = 8 * 1.5 * u * rms + 8 * terms ** 0.5 * 2.0 ** -23 * 8 * rms + u * ref.abs() * (1 + 2 * u) + sub
     assert ((ds.double() - ref).abs() <= tol).all()
+
+
+# ---------------------------------------------------------------- FP16's range, as the header states it
+@pytest.mark.gpu
+def test_fp16_weights_beyond_the_range():
+    """|s q| from 65520 on: exact up to 16 tokens, infinite where the weight is rounded to FP16"""
+    k, group = 64, 32
+    q = np.ones((3, k), np.int64)
+    q[:, 5] = -8
+    s = torch.tensor([[8184.0, 1.0], [8192.0, 1.0], [1.0, 0.5]], dtype=HF)
+    w = q * per_input(s, group, k)
+    for m in (4, 20):
+        x = torch.full((m, k), 2.0 ** -7, dtype=HF)
+        y = B.int4_linear(x.cuda(), store(q).cuda(), s.cuda(), group=group).cpu().double()
+        want = torch.from_numpy(x.double().numpy() @ w.T)
+        if m > 16:
+            want[:, 1] = float("-inf")
+        assert torch.equal(y, want.to(HF).double())
+    dx = B.int4_linear_dx(torch.full((2, 3), 2.0 ** -7, dtype=HF).cuda(), store(q).cuda(), s.cuda(), k, group=group).cpu()
+    assert (dx[:, 5] == float("-inf")).all() and torch.isfinite(dx[:, [i for i in range(k) if i != 5]]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("src", [BF, torch.float32])
+def test_fp16_scale_gradients_of_wider_activations(src):
+    """activations from 65520 on spoil their group, others up to 2^-25 add nothing; BF16 gradients take both"""
+    m, n, k, group = 8, 40, 384, 128
+    q = np.ones((n, k), np.int64)
+    x = torch.zeros(m, k)
+    x[:, :128], x[3, 40], x[:, 128:256], x[:, 256:] = 1.0, 1.0e5, 2.0 ** -27, 2.0 ** -26
+    x[:, 256] = 2.0 ** -10  # a group's largest; its others are far below it
+    act = B.act8_pack(x.to(src).cuda())
+    dy = torch.ones(m, n, device="cuda")
+    wide = B.int4_scale_grad(dy.to(BF), *act, store(q).cuda(), k, group=group).cpu()
+    c, a = act[0].cpu().double(), act[1].cpu().double().repeat_interleave(128, 1)
+    want = (c * a).view(m, 3, 128).sum((0, 2))
+    assert ((wide.double() - want).abs() <= 2 * 2.0 ** -8 * (1 + 2.0 ** -8) * want).all()  # a c and the result rounded
+    half = B.int4_scale_grad(dy.to(HF), *act, store(q).cuda(), k, group=group).cpu()
+    assert not torch.isfinite(half[:, 0]).any() and (half[:, 1] == 0).all()
+    assert ((half[:, 2].double() - m * 2.0 ** -10).abs() <= 2.0 ** -11 * m * 2.0 ** -10 * 2).all()
