@@ -382,3 +382,18 @@ def test_fp16_scale_gradients_of_wider_activations(src):
     half = B.int4_scale_grad(dy.to(HF), *act, store(q).cuda(), k, group=group).cpu()
     assert not torch.isfinite(half[:, 0]).any() and (half[:, 1] == 0).all()
     assert ((half[:, 2].double() - m * 2.0 ** -10).abs() <= 2.0 ** -11 * m * 2.0 ** -10 * 2).all()
+
+
+# ---------------------------------------------------------------- the forms with pairs of CTAs and with steps of 128
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("m,n,k,group", [(1100, 5100, 330, 32), (1100, 5100, 263, 128), (40, 5100, 1999, 32), (20, 5100, 1930, 64)])
+def test_infinite_scales_of_wide_forms(m, n, k, group, dtype):
+    test_infinite_scales(m, n, k, group, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("m,n,k,group", [(40, 5100, 1999, 32), (20, 5100, 1930, 64), (17, 19000, 1025, 32), (48, 5100, 1537, 128)])
+def test_ragged_steps_of_128(m, n, k, group, dtype):
+    test_linear_of_integers(m, n, k, group, dtype)
