@@ -303,7 +303,8 @@ class GroupedINT4Linear(nn.Module):
     requires_grad is set.  A layer built by the constructor holds a zero weight until quantize_weight
     runs or a checkpoint (codes, scales, bias) is loaded.  `status` (a buffer of one int32, not part of the
     checkpoint) stays 0 unless a kernel's wait ran out in a forward or backward since it was last zeroed: it then
-    holds EP_DEC_TIMEOUT (32), and those results are not valid."""
+    holds EP_DEC_TIMEOUT (32), and those results are not valid.  (DistributedDataParallel's broadcast of buffers
+    replaces it by the first rank's before each forward.)"""
 
     def __init__(self, in_features, out_features, bias=True, *, group=128, train_scales=False, device=None,
                  dtype=torch.bfloat16):
