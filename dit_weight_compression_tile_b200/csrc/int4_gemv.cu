@@ -74,33 +74,61 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
-// The sums of the elements of a warp's lanes in `bad` (of `o` and `t`), input by input as the formula has them, in
-// 64 bits: x[t, k] s[o, k / group] q[o, k], each lane every 32nd input, added across the warp in a fixed order.
-// For sums that came out infinite or NaN: an infinite scale times a group's sum hides an input whose product is
-// NaN, or is of the other sign, and sums of x q may pass fp32's range where the scale brings them back (BF16).
-// (Out of line: no call of finite sums pays for it.)
+// A sum `y` that came out infinite or NaN, by a warp.  It stands unless a scale of its feature is infinite (times a
+// group's sum, it hides an input whose product is NaN, or is of the other sign) or its token has finite activations
+// from 2^117 on (BF16: sums of x q may pass fp32's range where the scale brings them back).  Then it is taken again
+// input by input as the formula has it, x[t, k] (s[o, k / group] q[o, k]), each lane every 32nd input, added in a fixed
+// order: x as 2^-64 x and q as q / 16, so that nothing passes fp32's range whose result does not (activations below 2^-62
+// are lost beside those).  `last` and `huge`, kept by the caller: the token looked at last, and what was found.
+// 8192 x 28672, an infinity or NaN as the last input of each token: 25 us more for one, 0.34 ms for 16.
 template <typename T>
-__device__ __noinline__ float formula_sums(const Int4Args *a, uint32_t bad, uint32_t o, uint32_t t, float y) {
-    const uint32_t lane = threadIdx.x & 31u;
-    for (; bad; bad &= bad - 1) {
-        const uint32_t from = __ffs(bad) - 1;
-        const uint32_t row = __shfl_sync(0xffffffffu, o, from), token = __shfl_sync(0xffffffffu, t, from);
-        const uint32_t *codes = a->codes + int64_t(row) * a->words;
-        const uint16_t *scales = a->scales + int64_t(row) * a->groups, *x = a->x + int64_t(token) * a->ldx;
-        double sum = 0.0;
-        for (uint32_t k0 = 0; k0 < a->k; k0 += 32) {
-            const uint32_t k = k0 + lane, e = k & 7u;
-            if (k < a->k) {
-                const int q = int((__ldg(codes + k / 8) >> (4 * (e / 2) + 16 * (e & 1u))) & 15u) - 8;
-                sum += double(Elem<T>::f(__ldg(x + k))) * (double(Elem<T>::f(__ldg(scales + k / a->group))) * double(q));
+__device__ float formula_sum(const Int4Args &a, uint32_t o, uint32_t t, float y, uint32_t &last, bool &huge) {
+    constexpr uint32_t kAhead = 8;  // loads in flight
+    const uint32_t lane = threadIdx.x & 31u, group_bits = 31 - __clz(a.group);
+    const uint32_t *codes = a.codes + int64_t(o) * a.words;
+    const uint16_t *scales = a.scales + int64_t(o) * a.groups, *x = a.x + int64_t(t) * a.ldx;
+    if (Elem<T>::kInf == 0x7f80u && t != last) {
+        bool nan = false;  // (then y stands)
+        last = t;
+        huge = false;
+        for (uint32_t k0 = 0; k0 < a.k && !nan; k0 += 32 * kAhead) {
+            bool mine = false;
+#pragma unroll
+            for (uint32_t i = 0; i < kAhead; ++i) {
+                const uint32_t k = k0 + 32 * i + lane, u = k < a.k ? __ldg(x + k) & 0x7fffu : 0u;
+                mine |= u >= 0x7a00u && u < 0x7f80u;
+                nan |= u > 0x7f80u;
             }
-            if (__any_sync(0xffffffffu, sum != sum)) break;  // NaN stays
+            nan = __any_sync(0xffffffffu, nan);
+            huge |= __any_sync(0xffffffffu, mine);
+        }
+        if (nan) huge = false;
+    }
+    bool infinite = false;
+    for (uint32_t g = lane; g < a.groups; g += 32) infinite |= (__ldg(scales + g) & 0x7fffu) == Elem<T>::kInf;
+    if (!__any_sync(0xffffffffu, infinite) && !huge) return y;
+    float sum = 0.0f;
+    for (uint32_t k0 = 0; k0 < a.k; k0 += 32 * kAhead) {
+        uint32_t word[kAhead];
+        uint16_t xs[kAhead], ss[kAhead];
+#pragma unroll
+        for (uint32_t i = 0; i < kAhead; ++i) {
+            const uint32_t k = min(k0 + 32 * i + lane, a.k - 1);
+            word[i] = __ldg(codes + k / 8), xs[i] = __ldg(x + k), ss[i] = __ldg(scales + (k >> group_bits));
         }
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (lane == from) y = float(sum);
+        for (uint32_t i = 0; i < kAhead; ++i) {
+            const uint32_t k = k0 + 32 * i + lane, e = k & 7u, code = (word[i] >> (4 * (e / 2) + 16 * (e & 1u))) & 15u;
+            const float q = (__uint_as_float(0x4b000000u | code) - 8388616.0f) * 0.0625f;  // (2^23 + code) - (2^23 + 8)
+            const float w = Elem<T>::f(ss[i]) * q, v = Elem<T>::f(xs[i]);
+            // (a small v times an infinite w is infinite)
+            if (k < a.k) sum = fmaf(fabsf(w) == __uint_as_float(0x7f800000u) ? v : v * 0x1p-64f, w, sum);
+        }
+        if (__any_sync(0xffffffffu, sum != sum)) return __uint_as_float(0x7fffffffu);  // NaN stays
     }
-    return y;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    return sum * 0x1p68f;
 }
 
 struct GemvArgs {
@@ -328,20 +356,38 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_on_sm(RG)) int4_gemv_kernel(
     __syncthreads();
     // each feature's slices in order, the bias, one rounding
     const uint32_t rows = p.row_warps * p.rows;
-    for (uint32_t e0 = 32 * warp; e0 < rows * m; e0 += 32 * kWarps) {
-        const uint32_t e = e0 + lane, t = e / rows, f = e % rows, o = blockIdx.x * rows + f;
-        const bool mine = e < rows * m && o < a.n;
+    const auto joined = [&](uint32_t t, uint32_t f) {
         float y = 0.0f;
-        if (mine) {
-            for (uint32_t q = 0; q < slices; ++q) y += part[f / p.rows * slices + q][f % p.rows][t];
-            y *= Codes<T>::kUnit;
-        }
-        const uint32_t bad = __ballot_sync(0xffffffffu, mine && !(fabsf(y) < __uint_as_float(0x7f800000u)));
-        if (bad) y = formula_sums<T>(&p.a, bad, o, t, y);
-        if (!mine) continue;
+        for (uint32_t q = 0; q < slices; ++q) y += part[f / p.rows * slices + q][f % p.rows][t];
+        return y * Codes<T>::kUnit;
+    };
+    const auto finite = [](float y) { return fabsf(y) < __uint_as_float(0x7f800000u); };
+    const auto write = [&](uint32_t t, uint32_t o, float y) {
         if (a.bias) y += Elem<T>::f(__ldg(a.bias + o));
         a.out[int64_t(t) * a.n + o] = Elem<T>::bits(y);
+    };
+    bool bad = false;
+    for (uint32_t e = threadIdx.x; e < rows * m; e += 32 * kWarps) {
+        const uint32_t t = e / rows, f = e % rows, o = blockIdx.x * rows + f;
+        if (o >= a.n) continue;
+        const float y = joined(t, f);
+        if (finite(y)) write(t, o, y);
+        else bad = true;
     }
+    // the warp's others, one after the other
+    if (!__any_sync(0xffffffffu, bad)) return;
+    uint32_t last = ~0u;
+    bool huge = false;
+#pragma unroll 1
+    for (uint32_t e0 = 32 * warp; e0 < rows * m; e0 += 32 * kWarps)
+#pragma unroll 1
+        for (uint32_t e = e0; e < min(e0 + 32, rows * m); ++e) {
+            const uint32_t t = e / rows, f = e % rows, o = blockIdx.x * rows + f;
+            float y = joined(t, f);
+            if (o >= a.n || finite(y)) continue;
+            y = formula_sum<T>(a, o, t, y, last, huge);
+            if (lane == 0) write(t, o, y);
+        }
 }
 
 template <typename T, uint32_t GPB, uint32_t NT, uint32_t RG>

@@ -397,3 +397,45 @@ def test_infinite_scales_of_wide_forms(m, n, k, group, dtype):
 @pytest.mark.parametrize("m,n,k,group", [(40, 5100, 1999, 32), (20, 5100, 1930, 64), (17, 19000, 1025, 32), (48, 5100, 1537, 128)])
 def test_ragged_steps_of_128(m, n, k, group, dtype):
     test_linear_of_integers(m, n, k, group, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [1, 9, 17])
+def test_infinite_scales_of_the_smallest_and_largest_activations(m):
+    n, k, group = 20, 300, 64
+    q, _, s, x = case(n, k, group, BF, 12, m)
+    q[0] = 3
+    s[0, 1] = float("inf")
+    x[0] = 2.0 ** -126
+    x[m - 1, 290:] = 1e38  # in another group than the infinite scale's, sums of x q beyond fp32
+    s[:, 4] = 2.0 ** -30
+    x[m - 1, :290] = 2.0 ** -126
+    w = q * per_input(s, group, k)
+    with np.errstate(invalid="ignore"):
+        ref = (x.double().numpy()[:, None, :] * w[None]).sum(2)
+    y = B.int4_linear(x.cuda(), store(q).cuda(), s.cuda(), group=group).cpu()
+    assert ref[0, 0] == np.inf == ref[m - 1, 0]
+    same_infinities(y, ref)
+    xd = x.double().numpy()
+    check(y[:, 1:], ref[:, 1:], np.abs(xd) @ np.abs(w[1:]).T, np.abs(xd).sum(1, keepdims=True), k, BF)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("m", [1, 7, 16])
+@pytest.mark.parametrize("n,k,group,at", [(150, 700, 64, 699), (6001, 392, 32, 0), (5100, 300, 128, 299), (64, 8200, 128, 8000)])
+def test_tokens_with_nan_and_infinity_beside_others(m, n, k, group, at, dtype):
+    """each token's outputs are the formula's whatever the others hold, NaN and infinity at either end"""
+    q, codes, s, x = case(n, k, group, dtype, 13, m)
+    clean = B.int4_linear(x.cuda(), codes.cuda(), s.cuda(), group=group).cpu()
+    bad = x.clone()
+    bad[0, at] = float("nan")
+    if m > 1:
+        bad[m - 1, at], bad[m // 2, at] = float("inf"), float("-inf")
+    y = B.int4_linear(bad.cuda(), codes.cuda(), s.cuda(), group=group).cpu()
+    assert torch.isnan(y[0]).all()
+    rest = [t for t in range(1, m) if t not in (m - 1, m // 2)]
+    assert torch.equal(y[rest], clean[rest])
+    column = torch.from_numpy(q[:, at])
+    for t, sign in ((m - 1, 1), (m // 2, -1)) if m > 1 else ():
+        same_infinities(y[t], np.where(q[:, at] == 0, np.nan, np.copysign(np.inf, sign * column.double().numpy())))
