@@ -139,7 +139,7 @@ struct PackArgs {
 // subtract, on the pipe that has room.  Tiny a go by quotient_code.  With BF16 activations the quotients are
 // fractions of small numbers, and nine warps in ten have one next to a half: a slow path for all of those
 // took 34 us for 4096 x 8192, comparing and selecting 26 us, rintf and a conversion for each element, on a
-// half-rate pipe, 42 us.  This form takes 23.2 us (FP16 25.1; copying alone 16.3, the floor 15.6): the
+// half-rate pipe, 42 us.  This form takes 23.9 us (FP16 26.1; copying alone 16.3, the floor 15.6): the
 // instructions bound it (issue slots 79 %, ALU pipe 49 %, FMA pipe 43 % busy).  CTAs walk over the groups with the next one's
 // loads in flight.
 constexpr int kPackBlocks = 5;  // CTAs on an SM (4: the same; 6, with fewer registers: 27.6 us)

@@ -367,8 +367,12 @@ class GroupedINT4Linear(nn.Module):
         return B.int4_dequantize(self.codes, self.scales.detach(), self.in_features, self.group)
 
     def forward(self, x):
-        # (a layer pickled by an earlier version has no status)
-        return int4_group_linear(x, self.codes, self.scales, self.bias, self.group, self._buffers.get("status"))
+        codes, status = self._buffers["codes"], self._buffers.get("status")
+        # (a layer pickled by an earlier version has no status, one built on the meta device and given its tensors has
+        # it there still)
+        if status is not None and status.device != codes.device:
+            status = self.status = torch.zeros(1, dtype=torch.int32, device=codes.device)
+        return int4_group_linear(x, codes, self.scales, self.bias, self.group, status)
 
     def extra_repr(self):
         return (f"in_features={self.in_features}, out_features={self.out_features}, bias={self.bias is not None}, "

@@ -439,3 +439,15 @@ def test_tokens_with_nan_and_infinity_beside_others(m, n, k, group, at, dtype):
     column = torch.from_numpy(q[:, at])
     for t, sign in ((m - 1, 1), (m // 2, -1)) if m > 1 else ():
         same_infinities(y[t], np.where(q[:, at] == 0, np.nan, np.copysign(np.inf, sign * column.double().numpy())))
+
+
+@pytest.mark.gpu
+def test_a_layer_given_its_tensors_on_the_meta_device():
+    layer = GroupedINT4Linear.from_linear(torch.nn.Linear(96, 72, dtype=BF, device="cuda"), group=32)
+    x = torch.randn(20, 96, device="cuda").to(BF)
+    fresh = GroupedINT4Linear(96, 72, group=32, device="meta")
+    fresh.load_state_dict(layer.state_dict(), assign=True)
+    assert torch.equal(fresh(x), layer(x)) and fresh.status.device == x.device and fresh.status.tolist() == [0]
+    empty = GroupedINT4Linear(96, 72, group=32, device="meta").to_empty(device="cuda")
+    empty.load_state_dict(layer.state_dict())
+    assert torch.equal(empty(x), layer(x)) and empty.status.tolist() == [0]
